@@ -1,7 +1,7 @@
 """Build the CUDA library in-tree: tensor_gemm_reduce_gb300/lib/libgemm_rs.so.
 
-One nvcc invocation for sm_103a (tcgen05 / TMA need the arch-specific target).
-The library links the CUDA runtime statically and resolves the one driver call
+Sources compile for sm_103a (tcgen05 / TMA need the arch-specific target) side
+by side, one nvcc for each, and are linked into one library.  The library links the CUDA runtime statically and resolves the one driver call
 it needs (cuTensorMapEncodeTiled) at run time, so it has no link-time
 dependency on libcuda.
 """
@@ -11,20 +11,22 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libgemm_rs.so")
-SOURCES = [os.path.join(CSRC, "gemm_rs.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("kernels.cuh", "ptx.cuh", "schedule.h")] + [
-    os.path.join(ROOT, "include", "gemm_rs.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("gemm_rs.cu", "block_norm.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("kernels.cuh", "ptx.cuh", "schedule.h",
+                                                  "ops_common.cuh")] + [
+    os.path.join(ROOT, "include", f) for f in ("gemm_rs.h", "gemm_rs_ops.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
 ]
 
 
@@ -51,12 +53,22 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=None) 
         return LIB
     os.makedirs(LIBDIR, exist_ok=True)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc_path()] + NVCC_FLAGS + list(extra_flags or []) + ["-o", tmp] + SOURCES
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+    nvcc = [nvcc_path()] + NVCC_FLAGS + list(extra_flags or [])
+    with tempfile.TemporaryDirectory(prefix="gemm_rs_build_") as work:
+        objects = [os.path.join(work, os.path.basename(s) + ".o") for s in SOURCES]
+        steps = [[nvcc + ["-c", "-o", o, s] for o, s in zip(objects, SOURCES)],
+                 [nvcc + ["-shared", "-o", tmp] + objects]]
+        for cmds in steps:
+            if verbose:
+                print("\n".join(" ".join(c) for c in cmds), file=sys.stderr)
+            procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+                     for c in cmds]
+            outs = [p.communicate()[0] for p in procs]
+            for p, out in zip(procs, outs):
+                if p.returncode != 0:
+                    raise RuntimeError(f"nvcc failed ({p.returncode}):\n{out}")
+                if verbose and out:
+                    print(out, file=sys.stderr)
     os.replace(tmp, LIB)
     return LIB
 

@@ -1,0 +1,95 @@
+"""ctypes signatures of include/gemm_rs_ops.h and what its bindings share.
+
+The operators live in the same library as gemm_rs.py's and report the same
+status codes; a failure raises GemmRSError, a tensor of a wrong type, shape or
+device raises TypeError or ValueError before the library is called.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+import re
+from typing import Optional
+
+import torch
+
+from . import build as _build
+from . import gemm_rs as _g
+
+GemmRSError = _g.GemmRSError
+WORLD = _g.WORLD
+NORM_MAX_D = 16384
+
+_P, _I = ctypes.c_void_p, ctypes.c_int
+
+
+class gemm_rs_norm_desc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("D", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+# Every entry point declared in include/gemm_rs_ops.h.
+SIGS = {
+    "gemm_rs_norm_forward": [_P] * 10,
+    "gemm_rs_norm_workspace": [_P, _P],
+    "gemm_rs_norm_backward": [_P] * 16,
+}
+
+_LIB: Optional[ctypes.CDLL] = None
+
+
+def lib() -> ctypes.CDLL:
+    """The library with these entry points declared (built first if it is missing)."""
+    global _LIB
+    if _LIB is None:
+        cdll = _g.load_library()
+        for name, args in SIGS.items():
+            fn = getattr(cdll, name)
+            fn.restype, fn.argtypes = _I, args
+        _LIB = cdll
+    return _LIB
+
+
+def header_symbols():
+    """Names of the functions declared in include/gemm_rs_ops.h."""
+    text = open(os.path.join(_build.ROOT, "include", "gemm_rs_ops.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    return sorted(set(re.findall(r"\b(gemm_rs_[a-z0-9_]+)\s*\(", text)))
+
+
+def check(rc: int, what: str) -> None:
+    if rc != _g.GEMM_RS_OK:
+        raise GemmRSError(rc, what)
+
+
+def pointer(t, shape, dtype, name: str) -> int:
+    """Address of a contiguous CUDA tensor of this shape and dtype."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def distinct(outputs, inputs) -> None:
+    """Outputs must be buffers of their own (empty tensors have none)."""
+    seen = {p for p in inputs if p}
+    for p in outputs:
+        if p and p in seen:
+            raise ValueError("an output shares its buffer with another argument")
+        seen.add(p)
+
+
+def workspace_pointer(ws, need: int) -> int:
+    if ws is None or not ws.is_cuda or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"workspace missing or too small: {need} bytes of contiguous CUDA memory needed")
+    return ws.data_ptr()
+
+
+def stream_handle(stream, device) -> int:
+    """The stream's handle, or the current stream's of `device`, which must be the current device."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
