@@ -4,6 +4,8 @@
  *
  *   norm   the norms after and before a block, fused with the block's gate and
  *          residual scale, forward and backward
+ *   act8   the layer's input kept in 8 bits between the forward and the
+ *          backward pass, and the layer's backward pass from it (gemm_rs_bwd_*)
  *
  * Every device buffer and the CUDA stream belong to the caller; nothing here
  * allocates device memory or synchronises unless a comment says so.  Buffers
@@ -65,6 +67,46 @@ int gemm_rs_norm_backward(const gemm_rs_norm_desc* d, const void* dr, const void
                           const void* x, const void* y, const void* gate, const void* w_post,
                           const void* w_pre, const void* stats, void* dx, void* dy, void* dgate,
                           void* dw_post, void* dw_pre, void* workspace, void* stream);
+
+/* ------------------------------------------------------------------- act8
+ * An 8-bit checkpoint of A [8][M][K/8] bf16.  32 consecutive elements of a row
+ * (fewer at its end) share a power of two: 2^e with the least e >= -126 such
+ * that the largest magnitude is at most 127 * 2^e; each element is kept as
+ * round(a / 2^e) (to nearest even, at most 7 bits and a sign), so the restored
+ * value is exact in bf16.  (Magnitudes that would round to 2^128 keep the
+ * largest code below it.)  A group with an infinity or a NaN is restored as
+ * NaN throughout.
+ *
+ * codes: [8][M][pitch] bytes, scales: [8][M][pitch/32] bytes, pitch = K/8
+ * rounded up to 128; the contents of both are private to this library.
+ * Shapes as in gemm_rs.h: M % 8 == 0, K % 64 == 0; 0 allowed.
+ */
+int gemm_rs_act8_layout(int64_t M, int64_t K, int64_t* pitch, size_t* code_bytes,
+                        size_t* scale_bytes); /* host only */
+int gemm_rs_act8_save(int64_t M, int64_t K, const void* A, void* codes, void* scales,
+                      void* stream);
+int gemm_rs_act8_restore(int64_t M, int64_t K, const void* codes, const void* scales, void* A,
+                         void* stream);
+
+/* Backward pass of the row-parallel layer out = sum_r A_r W_r, with A from a
+ * checkpoint: for the output's gradient dY [M][N],
+ *   dA_r = dY W_r^T   [8][M][K/8]          dW_r = A_r^T dY   [8][K/8][N]
+ * bf16 in and out, fp32 accumulation, one rounding.  dA or dW may be NULL when
+ * it is not needed (W, or codes and scales, may then be NULL too). */
+typedef struct gemm_rs_bwd_plan_s* gemm_rs_bwd_t;
+
+/* timeout_ns: bound on every device-side wait; 0 = 2 s.  Shapes are checked
+ * before any CUDA call.  N % 8 == 0, the others as above. */
+int gemm_rs_bwd_create(int64_t M, int64_t N, int64_t K, uint64_t timeout_ns, gemm_rs_bwd_t* plan,
+                       size_t* workspace_bytes);
+/* The workspace may be uninitialised; the first call that sees a new pointer
+ * clears the control words at its end.  A plan serves one stream at a time. */
+int gemm_rs_bwd_run(gemm_rs_bwd_t plan, const void* dY, const void* W, const void* codes,
+                    const void* scales, void* dA, void* dW, void* workspace, void* stream);
+/* Synchronises `stream`; GEMM_RS_OK, GEMM_RS_ERR_TIMEOUT (a device-side wait
+ * gave up, the outputs are incomplete) or GEMM_RS_ERR_CUDA. */
+int gemm_rs_bwd_status(gemm_rs_bwd_t plan, void* stream);
+int gemm_rs_bwd_destroy(gemm_rs_bwd_t plan);
 
 #ifdef __cplusplus
 }

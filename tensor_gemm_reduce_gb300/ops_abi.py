@@ -20,7 +20,7 @@ GemmRSError = _g.GemmRSError
 WORLD = _g.WORLD
 NORM_MAX_D = 16384
 
-_P, _I = ctypes.c_void_p, ctypes.c_int
+_P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
 
 
 class gemm_rs_norm_desc(ctypes.Structure):
@@ -33,6 +33,13 @@ SIGS = {
     "gemm_rs_norm_forward": [_P] * 10,
     "gemm_rs_norm_workspace": [_P, _P],
     "gemm_rs_norm_backward": [_P] * 16,
+    "gemm_rs_act8_layout": [_L, _L, _P, _P, _P],
+    "gemm_rs_act8_save": [_L, _L, _P, _P, _P, _P],
+    "gemm_rs_act8_restore": [_L, _L, _P, _P, _P, _P],
+    "gemm_rs_bwd_create": [_L, _L, _L, ctypes.c_uint64, _P, _P],
+    "gemm_rs_bwd_run": [_P] * 9,
+    "gemm_rs_bwd_status": [_P, _P],
+    "gemm_rs_bwd_destroy": [_P],
 }
 
 _LIB: Optional[ctypes.CDLL] = None
