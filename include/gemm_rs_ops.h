@@ -6,6 +6,7 @@
  *          residual scale, forward and backward
  *   act8   the layer's input kept in 8 bits between the forward and the
  *          backward pass, and the layer's backward pass from it (gemm_rs_bwd_*)
+ *   w4     the layer for 1 to 32 tokens, with 4-bit weights and group scales
  *
  * Every device buffer and the CUDA stream belong to the caller; nothing here
  * allocates device memory or synchronises unless a comment says so.  Buffers
@@ -107,6 +108,36 @@ int gemm_rs_bwd_run(gemm_rs_bwd_t plan, const void* dY, const void* W, const voi
  * gave up, the outputs are incomplete) or GEMM_RS_ERR_CUDA. */
 int gemm_rs_bwd_status(gemm_rs_bwd_t plan, void* stream);
 int gemm_rs_bwd_destroy(gemm_rs_bwd_t plan);
+
+/* --------------------------------------------------------------------- w4
+ * The row-parallel layer for few tokens with 4-bit weights.  `group`
+ * consecutive inner elements of a rank's shard (32, 64 or 128; fewer at its
+ * end) share, for each column, a scale and optionally a zero point:
+ *
+ *   out[m][n] = sum_r sum_k x[r][m][k] (code[r][k][n] - zero[r][k/group][n]) scale[r][k/group][n]
+ *
+ * x [8][M][K/8] bf16, M from 0 to 32; codes [8][K/8][N] bytes 0..15 (the low
+ * four bits count); scales [8][ceil(K/8/group)][N] bf16; zeros of that shape,
+ * bytes 0..127 (the low seven bits count), or NULL for 8 everywhere; out [M][N]
+ * bf16.  Products are summed in fp32 in a fixed order and rounded once.
+ * N % 8 == 0, at most 2^22; K % 64 == 0.
+ *
+ * The weights are packed once into one buffer, whose contents are private to
+ * this library; codes, scales and zeros are not needed after that. */
+int gemm_rs_w4_bytes(int64_t N, int64_t K, int group, int has_zeros, size_t* weight_bytes,
+                     size_t* workspace_bytes); /* host only */
+/* Symmetric codes of W [8][K/8][N] bf16, rounded to nearest: scale =
+ * bf16(largest magnitude of the group / 7), code = 8 + round(w / scale) in
+ * 0..15; a group with an infinity or a NaN gets the scale NaN. */
+int gemm_rs_w4_quantize(int64_t N, int64_t K, int group, const void* W, void* codes, void* scales,
+                        void* stream);
+int gemm_rs_w4_pack(int64_t N, int64_t K, int group, const void* codes, const void* scales,
+                    const void* zeros, void* weight, void* stream);
+/* workspace: workspace_bytes (of any has_zeros), all zero before the first
+ * call; every call leaves its control words zero again.  Calls that can overlap
+ * on the GPU need workspaces of their own. */
+int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int has_zeros, const void* x,
+                   const void* weight, void* out, void* workspace, void* stream);
 
 #ifdef __cplusplus
 }

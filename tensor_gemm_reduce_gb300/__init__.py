@@ -4,7 +4,7 @@ The compute path is the CUDA library built from csrc/ (see build.py); the
 binding in gemm_rs.py is imported lazily so that the workload generator can be
 used without the library.
 """
-__all__ = ["workloads", "gemm_rs", "block_norm", "act8", "metrics", "build"]
+__all__ = ["workloads", "gemm_rs", "block_norm", "act8", "w4", "metrics", "build"]
 
 
 def __getattr__(name):

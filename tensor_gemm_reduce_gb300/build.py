@@ -18,7 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libgemm_rs.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("gemm_rs.cu", "block_norm.cu", "act8.cu", "backward.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("gemm_rs.cu", "block_norm.cu", "act8.cu", "backward.cu", "w4.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("kernels.cuh", "ptx.cuh", "schedule.h",
                                                   "ops_common.cuh", "act8.cuh")] + [
     os.path.join(ROOT, "include", f) for f in ("gemm_rs.h", "gemm_rs_ops.h")]
