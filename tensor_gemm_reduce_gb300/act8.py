@@ -28,16 +28,13 @@ class Checkpoint:
 
     def __init__(self, M: int, K: int, device=None):
         self.M, self.K = int(M), int(K)
+        self.shape = torch.Size((_a.WORLD, self.M, self.K // _a.WORLD))
         pitch, cb, sb = ctypes.c_int64(), ctypes.c_size_t(), ctypes.c_size_t()
         _a.check(_a.lib().gemm_rs_act8_layout(self.M, self.K, ctypes.byref(pitch), ctypes.byref(cb),
                                               ctypes.byref(sb)), "gemm_rs_act8_layout")
         device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
         self.codes = torch.empty(_a.WORLD, self.M, pitch.value, dtype=_U8, device=device)
         self.scales = torch.empty(_a.WORLD, self.M, pitch.value // GROUP, dtype=_U8, device=device)
-
-    @property
-    def shape(self):
-        return torch.Size((_a.WORLD, self.M, self.K // _a.WORLD))
 
     @property
     def nbytes(self) -> int:
@@ -48,13 +45,13 @@ def save(A, out: Checkpoint = None, stream=None) -> Checkpoint:
     """A checkpoint of A [8][M][K/8]; `out` is written when given."""
     if A.dim() != 3 or A.shape[0] != _a.WORLD:
         raise ValueError(f"A must have shape [{_a.WORLD}][M][K/{_a.WORLD}], got {tuple(A.shape)}")
-    a = _a.pointer(A, A.shape, _BF16, "A")
     if out is None:
         out = Checkpoint(A.shape[1], A.shape[2] * _a.WORLD, A.device)
     elif out.shape != A.shape:
         raise ValueError(f"the checkpoint holds {tuple(out.shape)}, A is {tuple(A.shape)}")
-    _a.check(_a.lib().gemm_rs_act8_save(out.M, out.K, a, out.codes.data_ptr(), out.scales.data_ptr(),
-                                        _a.stream_handle(stream, A.device)), "gemm_rs_act8_save")
+    rc = _a.ops().act8(A, out.codes, out.scales, False, None if stream is None else stream.cuda_stream)
+    if rc:
+        _a.check(rc, "gemm_rs_act8_save")
     return out
 
 
@@ -62,9 +59,11 @@ def restore(ck: Checkpoint, out=None, stream=None):
     """The bf16 values [8][M][K/8] that a checkpoint stands for."""
     if out is None:
         out = torch.empty(ck.shape, dtype=_BF16, device=ck.codes.device)
-    o = _a.pointer(out, ck.shape, _BF16, "out")
-    _a.check(_a.lib().gemm_rs_act8_restore(ck.M, ck.K, ck.codes.data_ptr(), ck.scales.data_ptr(), o,
-                                           _a.stream_handle(stream, out.device)), "gemm_rs_act8_restore")
+    elif out.shape != ck.shape:
+        raise ValueError(f"the checkpoint holds {tuple(ck.shape)}, out is {tuple(out.shape)}")
+    rc = _a.ops().act8(out, ck.codes, ck.scales, True, None if stream is None else stream.cuda_stream)
+    if rc:
+        _a.check(rc, "gemm_rs_act8_restore")
     return out
 
 
@@ -77,9 +76,8 @@ class BackwardPlan:
         h, ws = ctypes.c_void_p(), ctypes.c_size_t()
         _a.check(_a.lib().gemm_rs_bwd_create(self.M, self.N, self.K, timeout_ns, ctypes.byref(h),
                                              ctypes.byref(ws)), "gemm_rs_bwd_create")
-        self._h, self.workspace_bytes = h, ws.value
+        self._h, self.workspace_bytes = h.value, ws.value
         Kr = self.K // _a.WORLD
-        self.dy_shape = torch.Size((self.M, self.N))
         self.a_shape = torch.Size((_a.WORLD, self.M, Kr))
         self.w_shape = torch.Size((_a.WORLD, Kr, self.N))
 
@@ -90,20 +88,15 @@ class BackwardPlan:
     def run(self, dY, W, checkpoint, dA, dW, workspace, stream=None) -> None:
         """Enqueue one pass.  dA may be None (W is then not read), and so may dW (the
         checkpoint is then not read)."""
-        dy = _a.pointer(dY, self.dy_shape, _BF16, "dY")
-        w = codes = scales = da = dw = None
-        if dA is not None:
-            w = _a.pointer(W, self.w_shape, _BF16, "W")
-            da = _a.pointer(dA, self.a_shape, _BF16, "dA")
+        codes = scales = None
         if dW is not None:
             if checkpoint.shape != self.a_shape:
                 raise ValueError(f"the checkpoint holds {tuple(checkpoint.shape)}, the plan {tuple(self.a_shape)}")
-            codes, scales = checkpoint.codes.data_ptr(), checkpoint.scales.data_ptr()
-            dw = _a.pointer(dW, self.w_shape, _BF16, "dW")
-        ws = _a.workspace_pointer(workspace, self.workspace_bytes)
-        _a.distinct((da, dw, ws), (dy, w, codes, scales))
-        _a.check(_a.lib().gemm_rs_bwd_run(self._h, dy, w, codes, scales, da, dw, ws,
-                                          _a.stream_handle(stream, dY.device)), "gemm_rs_bwd_run")
+            codes, scales = checkpoint.codes, checkpoint.scales
+        rc = _a.ops().backward(self._h, self.M, self.N, self.K, self.workspace_bytes, dY, W, codes, scales, dA, dW,
+                               workspace, None if stream is None else stream.cuda_stream)
+        if rc:
+            _a.check(rc, "gemm_rs_bwd_run")
 
     def status(self, stream=None) -> int:
         """Synchronise the stream and report the device-side status of the last run."""

@@ -59,19 +59,11 @@ def new_workspace(x, gate=None):
 
 def forward(x, y, w_post, w_pre, gate=None, scale: float = 1.0, eps: float = 1e-6, out=None, stream=None):
     """Returns (r, h, stats); `out` takes the tensors of new_outputs()."""
-    d = _desc(x, gate, scale, eps)
-    shape, row = x.shape, w_post.shape
     r, h, stats = out if out is not None else new_outputs(x)
-    if row != shape[1:]:
-        raise ValueError(f"w_post must have shape {tuple(shape[1:])}, got {tuple(row)}")
-    ins = [_a.pointer(x, shape, _BF16, "x"), _a.pointer(y, shape, _BF16, "y"),
-           None if gate is None else _a.pointer(gate, gate.shape, _BF16, "gate"),
-           _a.pointer(w_post, row, _BF16, "w_post"), _a.pointer(w_pre, row, _BF16, "w_pre")]
-    outs = [_a.pointer(r, shape, _BF16, "r"), _a.pointer(h, shape, _BF16, "h"),
-            _a.pointer(stats, (2, shape[0]), _F32, "stats")]
-    _a.distinct(outs, ins)
-    _a.check(_a.lib().gemm_rs_norm_forward(ctypes.byref(d), *ins, *outs, _a.stream_handle(stream, x.device)),
-             "gemm_rs_norm_forward")
+    rc = _a.ops().norm_forward(x, y, w_post, w_pre, gate, scale, eps, r, h, stats,
+                               None if stream is None else stream.cuda_stream)
+    if rc:
+        _a.check(rc, "gemm_rs_norm_forward")
     return r, h, stats
 
 
@@ -80,23 +72,11 @@ def backward(dr, dh, x, y, w_post, w_pre, stats, gate=None, scale: float = 1.0, 
     """Gradients (dx, dy, dw_post, dw_pre, dgate) for dr and dh, the gradients of
     forward()'s r and h; stats as forward() returned them; dgate is None without
     a gate.  `out` takes the tensors of new_gradients()."""
-    d = _desc(x, gate, scale, 0.0)
-    shape, row = x.shape, x.shape[1:]
     dx, dy, dw_post, dw_pre, dgate = out if out is not None else new_gradients(x, gate)
     if workspace is None:
         workspace = new_workspace(x, gate)
-    ins = [_a.pointer(dr, shape, _BF16, "dr"), _a.pointer(dh, shape, _BF16, "dh"),
-           _a.pointer(x, shape, _BF16, "x"), _a.pointer(y, shape, _BF16, "y"),
-           None if gate is None else _a.pointer(gate, gate.shape, _BF16, "gate"),
-           _a.pointer(w_post, row, _BF16, "w_post"), _a.pointer(w_pre, row, _BF16, "w_pre"),
-           _a.pointer(stats, (2, shape[0]), _F32, "stats")]
-    if (dgate is None) != (gate is None):
-        raise ValueError("dgate must be given with a gate, and only then")
-    outs = [_a.pointer(dx, shape, _BF16, "dx"), _a.pointer(dy, shape, _BF16, "dy"),
-            None if gate is None else _a.pointer(dgate, gate.shape, _BF16, "dgate"),
-            _a.pointer(dw_post, row, _BF16, "dw_post"), _a.pointer(dw_pre, row, _BF16, "dw_pre")]
-    ws = _a.workspace_pointer(workspace, workspace_bytes(x, gate))
-    _a.distinct(outs + [ws], ins)
-    _a.check(_a.lib().gemm_rs_norm_backward(ctypes.byref(d), *ins, *outs, ws,
-                                            _a.stream_handle(stream, x.device)), "gemm_rs_norm_backward")
+    rc = _a.ops().norm_backward(dr, dh, x, y, w_post, w_pre, gate, stats, scale, dx, dy, dw_post, dw_pre, dgate,
+                                workspace, None if stream is None else stream.cuda_stream)
+    if rc:
+        _a.check(rc, "gemm_rs_norm_backward")
     return dx, dy, dw_post, dw_pre, dgate

@@ -1,4 +1,5 @@
-"""Build the CUDA library in-tree: tensor_gemm_reduce_gb300/lib/libgemm_rs.so.
+"""Build the CUDA library in-tree: tensor_gemm_reduce_gb300/lib/libgemm_rs.so,
+and the Python entry of its operators beside it (_ops.so).
 
 Sources compile for sm_103a (tcgen05 / TMA need the arch-specific target) side
 by side, one nvcc for each, and are linked into one library.  The library links the CUDA runtime statically and resolves the one driver call
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,9 @@ SOURCES = [os.path.join(CSRC, f) for f in ("gemm_rs.cu", "block_norm.cu", "act8.
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("kernels.cuh", "ptx.cuh", "schedule.h",
                                                   "ops_common.cuh", "act8.cuh")] + [
     os.path.join(ROOT, "include", f) for f in ("gemm_rs.h", "gemm_rs_ops.h")]
+
+BINDING = os.path.join(LIBDIR, "_ops.so")
+BINDING_SOURCE = os.path.join(CSRC, "ops_binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -40,16 +45,16 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _stale(target: str, sources) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in DEPS)
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(s) > t for s in sources)
 
 
 def build_library(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     """Compile the library if it is missing or older than its sources; return its path."""
-    if not force and not _stale():
+    if not force and not _stale(LIB, DEPS):
         return LIB
     os.makedirs(LIBDIR, exist_ok=True)
     tmp = LIB + f".tmp{os.getpid()}"
@@ -57,7 +62,7 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=None) 
     with tempfile.TemporaryDirectory(prefix="gemm_rs_build_") as work:
         objects = [os.path.join(work, os.path.basename(s) + ".o") for s in SOURCES]
         steps = [[nvcc + ["-c", "-o", o, s] for o, s in zip(objects, SOURCES)],
-                 [nvcc + ["-shared", "-o", tmp] + objects]]
+                 [nvcc + ["-shared", "-Xlinker", "-soname=libgemm_rs.so", "-o", tmp] + objects]]
         for cmds in steps:
             if verbose:
                 print("\n".join(" ".join(c) for c in cmds), file=sys.stderr)
@@ -73,5 +78,30 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=None) 
     return LIB
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/ops_binding.cpp against torch and the library; return its path."""
+    lib = build_library()
+    headers = [os.path.join(ROOT, "include", f) for f in ("gemm_rs.h", "gemm_rs_ops.h")]
+    if not force and not _stale(BINDING, [BINDING_SOURCE] + headers):
+        return BINDING
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-o", tmp, BINDING_SOURCE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    for inc in (sysconfig.get_paths()["include"], os.path.join(home, "include"),
+                os.path.join(home, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")):
+        cmd += ["-isystem", inc]
+    cmd += [lib, "-Wl,-rpath,$ORIGIN", "-L", os.path.join(home, "lib"), "-Wl,-rpath," + os.path.join(home, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
     print(build_library(force="--force" in sys.argv, verbose=True))
+    print(build_binding(force="--force" in sys.argv))

@@ -3,10 +3,16 @@
 The operators live in the same library as gemm_rs.py's and report the same
 status codes; a failure raises GemmRSError, a tensor of a wrong type, shape or
 device raises TypeError or ValueError before the library is called.
+
+Calls that a step makes go through a compiled entry (csrc/ops_binding.cpp):
+checking a call's tensors here took 8 to 11 us, longer than the smallest
+operators run.  What is called once (layouts, plans, packing) uses ctypes.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 from typing import Optional
@@ -61,6 +67,23 @@ def lib() -> ctypes.CDLL:
     return _LIB
 
 
+_OPS = None
+
+
+def ops():
+    """The compiled entry of the operators (built first if it is missing)."""
+    global _OPS
+    if _OPS is None:
+        lib()
+        path = _build.BINDING if os.path.exists(_build.BINDING) else _build.build_binding()
+        loader = importlib.machinery.ExtensionFileLoader("_ops", path)
+        spec = importlib.util.spec_from_file_location("_ops", path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _OPS = module
+    return _OPS
+
+
 def header_symbols():
     """Names of the functions declared in include/gemm_rs_ops.h."""
     text = open(os.path.join(_build.ROOT, "include", "gemm_rs_ops.h")).read()
@@ -84,23 +107,8 @@ def pointer(t, shape, dtype, name: str) -> int:
     return t.data_ptr()
 
 
-def distinct(outputs, inputs) -> None:
-    """Outputs must be buffers of their own (empty tensors have none)."""
-    seen = {p for p in inputs if p}
-    for p in outputs:
-        if p and p in seen:
-            raise ValueError("an output shares its buffer with another argument")
-        seen.add(p)
-
-
-def workspace_pointer(ws, need: int) -> int:
-    if ws is None or not ws.is_cuda or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
-        raise ValueError(f"workspace missing or too small: {need} bytes of contiguous CUDA memory needed")
-    return ws.data_ptr()
-
-
 def stream_handle(stream, device) -> int:
-    """The stream's handle, or the current stream's of `device`, which must be the current device."""
+    """The stream's handle, or the current stream's; `device` must be the current device."""
     if device.index != torch.cuda.current_device():
         raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
     return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream

@@ -75,18 +75,14 @@ def new_workspace(weight: Weight):
 
 def matvec(x, weight: Weight, out=None, workspace=None, stream=None):
     """out [M][N] = the layer's output for x [8][M][K/8], M at most 32."""
-    if x.dim() != 3:
-        raise ValueError(f"x must have shape [{_a.WORLD}][M][K/{_a.WORLD}], got {tuple(x.shape)}")
-    M = x.shape[1]
-    px = _a.pointer(x, (_a.WORLD, M, weight.K // _a.WORLD), _BF16, "x")
     if out is None:
-        out = torch.empty(M, weight.N, dtype=_BF16, device=x.device)
+        if x.dim() != 3:
+            raise ValueError(f"x must have shape [{_a.WORLD}][M][K/{_a.WORLD}], got {tuple(x.shape)}")
+        out = torch.empty(x.shape[1], weight.N, dtype=_BF16, device=x.device)
     if workspace is None:
         workspace = new_workspace(weight)
-    po = _a.pointer(out, (M, weight.N), _BF16, "out")
-    ws = _a.workspace_pointer(workspace, weight.workspace_bytes)
-    _a.distinct((po, ws), (px, weight.data.data_ptr()))
-    _a.check(_a.lib().gemm_rs_w4_run(M, weight.N, weight.K, weight.group, weight.has_zeros, px,
-                                     weight.data.data_ptr(), po, ws, _a.stream_handle(stream, x.device)),
-             "gemm_rs_w4_run")
+    rc = _a.ops().w4_matvec(x, weight.N, weight.K, weight.group, weight.has_zeros, weight.data, out, workspace,
+                            None if stream is None else stream.cuda_stream)
+    if rc:
+        _a.check(rc, "gemm_rs_w4_run")
     return out

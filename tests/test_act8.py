@@ -245,6 +245,9 @@ def test_tensor_refusals():
         plan.run(dY, W, ck, dA, dW, ws[:16])
     plan.run(dY, W, ck, dA, dW, ws)
     assert plan.status() == G.GEMM_RS_OK
+    plan.close()
+    with pytest.raises(ValueError):
+        plan.run(dY, W, ck, dA, dW, ws)
 
 
 # ---------------------------------------------------------------- no GPU needed
