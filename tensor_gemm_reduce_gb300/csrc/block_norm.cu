@@ -1,6 +1,7 @@
 // block_norm.cu -- the norms after and before a block, fused with the block's
 // gate and residual scale, forward and backward (gemm_rs_norm_* in
 // include/gemm_rs_ops.h).
+#include <atomic>
 #include <cmath>
 
 #include "ops_common.cuh"
@@ -10,13 +11,61 @@ using namespace grs;
 namespace {
 
 constexpr int kMaxThreads = 512;
-// Row chunks of the backward pass: one per SM of a GB300.  A constant, so that
-// the workspace size and the order of the sums do not depend on the device.
-constexpr int kChunks = 152;
+constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kMaxSmem = 200 * 1024;  // of 227 KB; the rest stays L1 for the weights
+// The backward pass cuts the rows into at most kBlocks x groups chunks, one
+// block per SM of a GB300.  A constant, so that the workspace size and the
+// order of the sums do not depend on the device.
+constexpr int kBlocks = 152;
+
+// A row belongs to a group of `warps` warps, thread t of the group holding its
+// 16-byte vectors t, t + 32 warps, ... (`v` of them at most); a block has
+// `groups` such groups, each with rows of its own.  Every thread copies the
+// vectors that it will use into a ring of `stages` rows in shared memory with
+// cp.async, so rows arrive while earlier ones are worked on, without registers
+// for them and without a barrier: a thread waits for its own copies only.
+struct Shape {
+  int v, warps, groups, stages, smem;
+};
+Shape shape_of(int nv, int arrays, long long rows, int blocks, int budget, int extra_per_vector) {
+  Shape s = {0, 0, 0, 0, 0};
+  // Two vectors a thread unless that leaves more than a quarter of the warps out.
+  int best = 0;
+  for (int v : {2, 3, 1, 4}) {
+    if (nv <= 32) v = 1;
+    const int warps = (nv + 32 * v - 1) / (32 * v);
+    if (warps > kMaxWarps) continue;
+    const int groups = kMaxWarps / warps;
+    const int used = groups * warps;
+    if (used > best) {
+      best = used;
+      s.v = v;
+      s.warps = warps;
+      s.groups = groups;
+      if (used >= kMaxWarps * 3 / 4) break;
+    }
+  }
+  // few rows: spread them over the blocks first
+  const long long need = (rows + blocks - 1) / blocks;
+  if (s.groups > need) s.groups = need < 1 ? 1 : (int)need;
+  const int row = s.groups * nv * 16;
+  const int extra = s.groups * nv * extra_per_vector;
+  s.stages = (budget - extra) / (arrays * row);
+  if (s.stages > 4) s.stages = 4;
+  if (s.stages < 1) s.stages = 1;
+  s.smem = s.stages * arrays * row + extra;
+  return s;
+}
+
+// Where the gate comes from: one row (or none) is held in registers like the
+// weights; a row for some rows each (kSequence) or for each row (kElement)
+// goes through the ring with the row's other inputs.
+enum GateMode : int { kSingle = 0, kSequence = 1, kElement = 2 };
 
 struct NormParams {
   long long M;
-  int D, nv;            // nv = D / 8 vectors of 16 bytes in a row
+  int D, nv;                // nv = D / 8 vectors of 16 bytes in a row
+  int warps, groups, stages;
   long long rows_per_gate;  // M / gate_rows
   float scale, eps, inv_d;
   const uint4 *x, *y, *gate, *w_post, *w_pre;
@@ -25,64 +74,150 @@ struct NormParams {
   // backward
   const uint4 *dr, *dh;
   uint4 *dx, *dy, *dgate, *dw_post, *dw_pre;
-  long long chunk_rows;
-  int chunks;
-  float *part_s, *part_pre, *part_post, *part_gate;
+  long long chunk_rows;  // consecutive rows of a group
+  int chunks, blocks;
+  float *part_post, *part_pre, *part_gate;
 };
 
-// Threads take whole 16-byte vectors of a row: thread t vectors t, t + T, ...
-// (V of them at most).  T is the least number of warps that covers the row
-// with V vectors each.
-int vectors_per_thread(int nv) { return (nv + kMaxThreads - 1) / kMaxThreads; }
-int threads_for(int nv, int v) { return ((nv + v - 1) / v + 31) / 32 * 32; }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most `stages` - 1 of this thread's copy groups are pending.
+__device__ __forceinline__ void cp_async_wait(int stages) {
+  if (stages >= 4)
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (stages == 3)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (stages == 2)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 
-// One row at a time: both sums are block-wide, the row stays in registers.
-template <int V>
-__global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormParams p) {
-  __shared__ float part[2][32];
-  const int t = threadIdx.x, T = blockDim.x;
-  for (long long m = blockIdx.x; m < p.M; m += gridDim.x) {
-    const uint4* xr = p.x + m * p.nv;
-    const uint4* yr = p.y + m * p.nv;
-    const uint4* gr = p.gate ? p.gate + (m / p.rows_per_gate) * p.nv : nullptr;
-    float r[V][8], y[V][8];
-    float s[1] = {0.f};
+// Sums over a group, in each of its threads.  `part` holds kMaxWarps * N
+// floats of this group; a group alternates between two of them, so that one
+// barrier a sum is enough.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float* part, int warps, int group) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int i = t + v * T;
-      const bool in = i < p.nv;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      unpack8(in ? yr[i] : zero, y[v]);
-      unpack8(in ? xr[i] : zero, r[v]);
+  for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] = fmaf(y[v][j], y[v][j], s[0]);
-    }
-    block_sum<1>(s, part[0]);
-    const float pn = 1.f / sqrtf(fmaf(s[0], p.inv_d, p.eps));
-    s[0] = 0.f;
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (warps == 1) return;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - group * warps;
+  if (lane == 0)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int i = t + v * T;
-      if (i < p.nv) {
-        float w[8], g[8];
-        unpack8(__ldg(p.w_post + i), w);
-        if (gr) unpack8(__ldg(gr + i), g);
+    for (int i = 0; i < N; ++i) part[i * kMaxWarps + warp] = v[i];
+  asm volatile("barrier.sync.aligned %0, %1;" ::"r"(group + 1), "r"(32 * warps) : "memory");
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float u = y[v][j] * pn * w[j];
-          r[v][j] = fmaf(gr ? p.scale * g[j] : p.scale, u, r[v][j]);
-          s[0] = fmaf(r[v][j], r[v][j], s[0]);
+  for (int i = 0; i < N; ++i) {
+    const int w = lane % kMaxWarps;  // both halves of the warp add the same values
+    v[i] = w < warps ? part[i * kMaxWarps + w] : 0.f;
+  }
+#pragma unroll
+  for (int o = kMaxWarps / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+}
+
+// Blocks of the forward kernel that share an SM: with up to two vectors a
+// thread 64 registers are enough.
+constexpr int forward_blocks(int v) { return v <= 2 ? 2 : 1; }
+
+// Both sums are over the group, the row stays in registers.
+template <int V, bool kManyGates>
+__global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_kernel(const NormParams p) {
+  extern __shared__ uint4 ring[];
+  __shared__ float part[kMaxWarps][2][kMaxWarps];
+  constexpr int kArrays = kManyGates ? 3 : 2;
+  const int group = (int)(threadIdx.x >> 5) / p.warps, T = 32 * p.warps;
+  const int t = threadIdx.x - group * T;
+  const uint32_t mine = smem_u32(ring) + 16u * (group * p.nv + t);
+  const uint32_t plane = 16u * p.groups * p.nv;  // one array of a stage
+  const long long step = (long long)gridDim.x * p.groups;
+  long long m = (long long)blockIdx.x * p.groups + group;
+  griddep_wait();
+
+  auto fetch = [&](long long row, int stage) {
+    if (row < p.M) {
+      const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
+      const uint4* gr = kManyGates ? p.gate + (row / p.rows_per_gate) * p.nv : nullptr;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int i = t + v * T;
+        if (i < p.nv) {
+          cp_async16(base + 16u * v * T, p.y + row * p.nv + i);
+          cp_async16(base + plane + 16u * v * T, p.x + row * p.nv + i);
+          if (kManyGates) cp_async16(base + 2 * plane + 16u * v * T, gr + i);
         }
       }
     }
-    block_sum<1>(s, part[1]);
+    cp_async_commit();
+  };
+  for (int s = 0; s < p.stages; ++s) fetch(m + s * step, s);
+  // w_post, times scale and the gate when there is one row of it
+  float gw[V][8];
+  uint4 wq[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = t + v * T;
+    if (i < p.nv) {
+      unpack8(__ldg(p.w_post + i), gw[v]);
+      wq[v] = __ldg(p.w_pre + i);
+      float g[8];
+      if (!kManyGates && p.gate) unpack8(__ldg(p.gate + i), g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) gw[v][j] *= !kManyGates && p.gate ? p.scale * g[j] : p.scale;
+    }
+  }
+
+  int stage = 0;
+  for (; m < p.M; m += step) {
+    cp_async_wait(p.stages);
+    const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
+    float r[V][8];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (t + v * T < p.nv) {
+        float y[8];
+        unpack8(ld_shared_v4(base + 16u * v * T), y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[0] = fmaf(y[j], y[j], s[0]);
+      }
+    group_sum<1>(s, part[group][0], p.warps, group);
+    const float pn = 1.f / sqrtf(fmaf(s[0], p.inv_d, p.eps));
+    s[0] = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (t + v * T < p.nv) {
+        float y[8], g[8];
+        unpack8(ld_shared_v4(base + 16u * v * T), y);
+        unpack8(ld_shared_v4(base + plane + 16u * v * T), r[v]);
+        if (kManyGates) unpack8(ld_shared_v4(base + 2 * plane + 16u * v * T), g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float u = y[j] * pn * gw[v][j];
+          r[v][j] = kManyGates ? fmaf(g[j], u, r[v][j]) : r[v][j] + u;
+          s[0] = fmaf(r[v][j], r[v][j], s[0]);
+        }
+      }
+    fetch(m + p.stages * step, stage);  // the row is in registers: its slot is free
+    if (++stage == p.stages) stage = 0;
+    group_sum<1>(s, part[group][1], p.warps, group);
     const float qn = 1.f / sqrtf(fmaf(s[0], p.inv_d, p.eps));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = t + v * T;
       if (i < p.nv) {
         float w[8], h[8];
-        unpack8(__ldg(p.w_pre + i), w);
+        unpack8(wq[v], w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[j] = r[v][j] * qn * w[j];
         p.r[m * p.nv + i] = pack8(r[v]);
@@ -101,54 +236,103 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormPar
 //   t  = dr + q (a - rn m1)                       dx = t
 //   dy = p (scale gate t w_post - yn m2),         m2 = mean(scale gate t w_post yn)
 //                                                    = mean(c (dr + q a)) - q m1 mean(c rn)
-// so one block-wide sum of three values serves both norms.
-// Each block owns chunk_rows consecutive rows and its threads own columns, so
-// the sums over rows stay in registers: S = sum of t yn over the rows of one
-// gate row, which gives both dgate = scale w_post S and that gate row's share
-// scale gate S of dw_post; and sum of dh rn = dw_pre.  kMultiGate: several
-// gate rows, so dw_post has an accumulator of its own.  A gate row whose rows
-// all lie in the chunk is written at once; one that crosses a chunk border
-// leaves a partial sum in slot 2 c (its rows begin at the chunk's first row or
-// before) or 2 c + 1.
-template <int V, bool kMultiGate>
-__global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormParams p) {
-  __shared__ float part[2][96];
-  const int t = threadIdx.x, T = blockDim.x, c = blockIdx.x;
+// so one sum of three values over the row serves both norms.
+// Each group owns chunk_rows consecutive rows and its threads own columns, so
+// the sums over rows stay in registers: the sum of t yn over the rows of one
+// gate row gives both dgate = scale w_post S and that gate row's share
+// scale gate S of dw_post; the sum of dh rn is dw_pre.  kSequence adds the
+// shares of dw_post in shared memory, at the end of each gate row; kElement
+// has no S.  A gate row whose rows all lie in the chunk is written at once;
+// one that crosses a chunk border leaves a partial sum in slot 2 c (its rows
+// begin at the chunk's first row or before) or 2 c + 1.  At the end the
+// block's groups are added and the block writes one row of partial sums.
+template <int V, int kMode>
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const NormParams p) {
+  extern __shared__ uint4 ring[];
+  __shared__ float part[kMaxWarps][2][3 * kMaxWarps];
+  constexpr int kArrays = kMode == kSingle ? 4 : 5;
+  const int group = (int)(threadIdx.x >> 5) / p.warps, T = 32 * p.warps;
+  const int t = threadIdx.x - group * T;
+  const uint32_t mine = smem_u32(ring) + 16u * (group * p.nv + t);
+  const uint32_t plane = 16u * p.groups * p.nv;
+  // kSequence: this thread's columns of dw_post, after the ring
+  float* post = reinterpret_cast<float*>(ring + (size_t)p.stages * kArrays * p.groups * p.nv) + 8 * (group * p.nv + t);
+  const long long c = (long long)blockIdx.x * p.groups + group;
   const long long m0 = c * p.chunk_rows;
   const long long m1 = m0 + p.chunk_rows < p.M ? m0 + p.chunk_rows : p.M;
-  float S[V][8], Ppre[V][8], Ppost[kMultiGate ? V : 1][8];
+  griddep_wait();
+
+  auto fetch = [&](long long row, int stage) {
+    if (row < m1) {
+      const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
+      const uint4* gr = kMode != kSingle ? p.gate + (row / p.rows_per_gate) * p.nv : nullptr;
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      S[v][j] = Ppre[v][j] = 0.f;
-      if (kMultiGate) Ppost[v][j] = 0.f;
+      for (int v = 0; v < V; ++v) {
+        const int i = t + v * T;
+        if (i < p.nv) {
+          const uint32_t dst = base + 16u * v * T;
+          cp_async16(dst, p.y + row * p.nv + i);
+          cp_async16(dst + plane, p.x + row * p.nv + i);
+          cp_async16(dst + 2 * plane, p.dr + row * p.nv + i);
+          cp_async16(dst + 3 * plane, p.dh + row * p.nv + i);
+          if (kMode != kSingle) cp_async16(dst + 4 * plane, gr + i);
+        }
+      }
     }
+    cp_async_commit();
+  };
+  for (int s = 0; s < p.stages; ++s) fetch(m0 + s, s);
+
+  float gw[V][8];  // scale w_post, times the gate when there is one row of it
+  uint4 wq[V];
+  float S[V][8], Ppre[V][8];  // kElement: S is this thread's sum for dw_post
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = t + v * T;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) S[v][j] = Ppre[v][j] = 0.f;
+    if (i < p.nv) {
+      unpack8(__ldg(p.w_post + i), gw[v]);
+      wq[v] = __ldg(p.w_pre + i);
+      float g[8];
+      if (kMode == kSingle && p.gate) unpack8(__ldg(p.gate + i), g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        gw[v][j] *= kMode == kSingle && p.gate ? p.scale * g[j] : p.scale;
+        if (kMode == kSequence) post[8 * v * T + j] = 0.f;
+      }
+    }
+  }
+
+  int stage = 0;
   for (long long m = m0; m < m1; ++m) {
-    const float pn = p.stats[m], qn = p.stats[p.M + m];
-    const long long gi = p.gate ? m / p.rows_per_gate : 0;
-    const uint4* gr = p.gate ? p.gate + gi * p.nv : nullptr;
+    const float pn = __ldg(p.stats + m), qn = __ldg(p.stats + p.M + m);
+    cp_async_wait(p.stages);
+    const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
     float yn[V][8], rn[V][8], z[V][8];  // z = dr + q a
+    uint4 gp[V];                        // this row's gate
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int i = t + v * T;
-      if (i < p.nv) {
-        float x[8], w[8], g[8], dh[8], dr[8], wq[8];
-        unpack8(p.y[m * p.nv + i], yn[v]);
-        unpack8(p.x[m * p.nv + i], x);
-        unpack8(p.dr[m * p.nv + i], dr);
-        unpack8(p.dh[m * p.nv + i], dh);
-        unpack8(__ldg(p.w_post + i), w);
-        unpack8(__ldg(p.w_pre + i), wq);
-        if (gr) unpack8(__ldg(gr + i), g);
+      if (t + v * T < p.nv) {
+        const uint32_t src = base + 16u * v * T;
+        float x[8], g[8], dh[8], w[8];
+        unpack8(ld_shared_v4(src), yn[v]);
+        unpack8(ld_shared_v4(src + plane), x);
+        unpack8(ld_shared_v4(src + 2 * plane), z[v]);
+        unpack8(ld_shared_v4(src + 3 * plane), dh);
+        unpack8(wq[v], w);
+        if (kMode != kSingle) {
+          gp[v] = ld_shared_v4(src + 4 * plane);
+          unpack8(gp[v], g);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           yn[v][j] *= pn;
-          const float br = (gr ? p.scale * g[j] : p.scale) * (yn[v][j] * w[j]);
+          const float br = (kMode != kSingle ? g[j] * gw[v][j] : gw[v][j]) * yn[v][j];
           rn[v][j] = (x[j] + br) * qn;
-          const float a = dh[j] * wq[j];
-          z[v][j] = fmaf(qn, a, dr[j]);
+          const float a = dh[j] * w[j];
+          z[v][j] = fmaf(qn, a, z[v][j]);
           Ppre[v][j] = fmaf(dh[j], rn[v][j], Ppre[v][j]);
           s[0] = fmaf(a, rn[v][j], s[0]);
           s[1] = fmaf(br, z[v][j], s[1]);
@@ -156,34 +340,41 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormPa
         }
       }
     }
-    block_sum<3>(s, part[m & 1]);
+    fetch(m + p.stages, stage);  // the row is in registers: its slot is free
+    if (++stage == p.stages) stage = 0;
+    group_sum<3>(s, part[group][m & 1], p.warps, group);
     const float k1 = qn * (s[0] * p.inv_d);                 // q m1
     const float k2 = fmaf(-k1, s[2], s[1]) * p.inv_d * pn;  // p m2
-    const bool last = !kMultiGate || m + 1 == m1 || (m + 1) % p.rows_per_gate == 0;
+    const long long gi = kMode == kSequence ? m / p.rows_per_gate : m;
+    const bool last = kMode == kSequence && (m + 1 == m1 || (m + 1) % p.rows_per_gate == 0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = t + v * T;
       if (i < p.nv) {
-        float w[8], g[8], dx[8], dy[8];
-        unpack8(__ldg(p.w_post + i), w);
-        if (gr) unpack8(__ldg(gr + i), g);
+        float g[8], dx[8], dy[8], dg[8];
+        if (kMode != kSingle) unpack8(gp[v], g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float tt = fmaf(-k1, rn[v][j], z[v][j]);
-          const float gs = gr ? p.scale * g[j] : p.scale;
+          const float ty = tt * yn[v][j];
           dx[j] = tt;
-          S[v][j] = fmaf(tt, yn[v][j], S[v][j]);
-          dy[j] = fmaf(pn * (gs * tt), w[j], -k2 * yn[v][j]);
+          dy[j] = fmaf(pn * tt, kMode != kSingle ? g[j] * gw[v][j] : gw[v][j], -k2 * yn[v][j]);
+          if (kMode == kElement) {
+            dg[j] = gw[v][j] * ty;
+            S[v][j] = fmaf(g[j], ty, S[v][j]);
+          } else {
+            S[v][j] += ty;
+          }
         }
         p.dx[m * p.nv + i] = pack8(dx);
         p.dy[m * p.nv + i] = pack8(dy);
-        if (kMultiGate && last) {  // end of a gate row's rows in this chunk
+        if (kMode == kElement) p.dgate[m * p.nv + i] = pack8(dg);
+        if (kMode == kSequence && last) {  // end of a gate row's rows in this chunk
           const long long first = gi * p.rows_per_gate;
           if (first >= m0 && first + p.rows_per_gate <= m1) {
-            float o[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = p.scale * w[j] * S[v][j];
-            p.dgate[gi * p.nv + i] = pack8(o);
+            for (int j = 0; j < 8; ++j) dg[j] = gw[v][j] * S[v][j];
+            p.dgate[gi * p.nv + i] = pack8(dg);
           } else {
             float* slot = p.part_gate + (2 * c + (first > m0 ? 1 : 0)) * (long long)p.D + 8 * i;
 #pragma unroll
@@ -191,66 +382,88 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const NormPa
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            Ppost[v][j] = fmaf(p.scale * g[j], S[v][j], Ppost[v][j]);
+            post[8 * v * T + j] = fmaf(g[j], S[v][j], post[8 * v * T + j]);
             S[v][j] = 0.f;
           }
         }
       }
     }
   }
+  griddep_launch_dependents();
+
+  // add the block's groups; the ring is free once every thread is here
+  if (kMode == kSequence)
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int i = t + v * T;
-    if (i < p.nv)
+    for (int v = 0; v < V; ++v)
+      if (t + v * T < p.nv)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const long long at = (long long)c * p.D + 8 * i + j;
-        p.part_pre[at] = Ppre[v][j];
-        if (kMultiGate)
-          p.part_post[at] = Ppost[v][j];
-        else
-          p.part_s[at] = S[v][j];
+        for (int j = 0; j < 8; ++j) S[v][j] = post[8 * v * T + j];
+  float* sums = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float* out = (which ? p.part_pre : p.part_post) + (long long)blockIdx.x * p.D;
+    if (p.groups == 1) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int i = t + v * T;
+        if (i < p.nv) {
+          const float(&f)[8] = which ? Ppre[v] : S[v];
+          reinterpret_cast<float4*>(out)[2 * i] = make_float4(f[0], f[1], f[2], f[3]);
+          reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
       }
+      continue;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = t + v * T;
+      if (i < p.nv)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[group * p.D + 8 * i + j] = which ? Ppre[v][j] : S[v][j];
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
+      float f = 0.f;
+      for (int k = 0; k < p.groups; ++k) f += sums[k * p.D + d];
+      out[d] = f;
+    }
   }
 }
 
-// Joins the chunks' sums, 32 columns a block: warp w adds chunks w, w + 8, ...
+// Joins the blocks' sums, 32 columns a block: warp w adds rows w, w + 8, ...
 // and the eight sums are added in order.  blockIdx.y: 0 dw_pre, 1 dw_post (and
-// dgate when there is one gate row), 2 + b the gate row that crosses the border
-// between chunks b and b + 1 first (each crossing row has one first border).
-__global__ void __launch_bounds__(256) norm_join_kernel(const NormParams p, int multi) {
+// dgate when there is one gate row), from 2 on the gate rows that cross a chunk
+// border: gate row blockIdx.y - 2 if there are fewer gate rows than chunks,
+// else the one that crosses the border after chunk blockIdx.y - 2 as its first.
+__global__ void __launch_bounds__(256) norm_join_kernel(const NormParams p, int many_gates, int by_gate) {
   __shared__ float part[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   const bool in = col < p.D;
   const int job = blockIdx.y;
+  griddep_wait();
   const float* src;
-  int n = p.chunks;                       // rows of src to add, `step` apart
+  int n = p.blocks;  // rows of src to add, `step` apart
   long long step = p.D, gi = 0;
+  bool odd = false;
   if (job == 0) {
     src = p.part_pre;
   } else if (job == 1) {
-    src = multi ? p.part_post : p.part_s;
+    src = p.part_post;
   } else {
-    const int b = job - 2;
-    const long long border = (long long)(b + 1) * p.chunk_rows;
-    gi = border / p.rows_per_gate;
-    const long long first = gi * p.rows_per_gate;
-    if (first == border || first / p.chunk_rows != b) return;
-    const long long last = first + p.rows_per_gate - 1;
-    n = (int)(last / p.chunk_rows) - b + 1;
-    src = p.part_gate + 2ll * b * p.D;
+    gi = by_gate ? job - 2 : (job - 1) * p.chunk_rows / p.rows_per_gate;
+    const long long first = gi * p.rows_per_gate, last = first + p.rows_per_gate - 1;
+    const long long b = first / p.chunk_rows;
+    if (last / p.chunk_rows == b || (!by_gate && b != job - 2)) return;
+    n = (int)(last / p.chunk_rows - b) + 1;
+    src = p.part_gate + 2 * b * p.D;
     step = 2ll * p.D;
-    // chunk b's slot is the odd one when the gate row begins after its first row
-    if (first > b * p.chunk_rows) src += p.D;
+    odd = first > b * p.chunk_rows;  // chunk b's slot; the later chunks' are even
   }
   float s = 0.f;
   if (in)
-    for (int k = warp; k < n; k += 8) {
-      long long at = k * step;
-      if (job >= 2 && k > 0 && src != p.part_gate + 2ll * (job - 2) * p.D) at -= p.D;
-      s += src[at + col];
-    }
+    for (int k = warp; k < n; k += 8) s += src[k * step + (odd && k == 0 ? p.D : 0) + col];
   part[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || !in) return;
@@ -265,8 +478,8 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const NormParams p, int 
   };
   if (job == 0) {
     put(p.dw_pre, col, s);
-  } else if (job == 1 && multi) {
-    put(p.dw_post, col, s);
+  } else if (job == 1 && many_gates) {
+    put(p.dw_post, col, p.scale * s);
   } else if (job == 1) {
     put(p.dw_post, col, p.gate ? p.scale * bf(p.gate, col) * s : p.scale * s);
     if (p.gate) put(p.dgate, col, p.scale * bf(p.w_post, col) * s);
@@ -285,15 +498,25 @@ int check(const gemm_rs_norm_desc* d) {
   return GEMM_RS_OK;
 }
 
+GateMode mode_of(const gemm_rs_norm_desc* d) {
+  return d->gate_rows <= 1 ? kSingle : d->gate_rows == d->M ? kElement : kSequence;
+}
+
+// How the backward pass cuts the rows: a function of the sizes alone.
 struct Split {
+  Shape shape;
   long long chunk_rows;
-  int chunks;
+  int chunks, blocks;
 };
 Split split_of(const gemm_rs_norm_desc* d) {
   Split s;
-  s.chunk_rows = (d->M + kChunks - 1) / kChunks;
+  const GateMode mode = mode_of(d);
+  s.shape = shape_of((int)(d->D / 8), mode == kSingle ? 4 : 5, d->M, kBlocks, kMaxSmem, mode == kSequence ? 32 : 0);
+  const long long lanes = (long long)kBlocks * s.shape.groups;
+  s.chunk_rows = (d->M + lanes - 1) / lanes;
   if (s.chunk_rows < 1) s.chunk_rows = 1;
   s.chunks = (int)((d->M + s.chunk_rows - 1) / s.chunk_rows);
+  s.blocks = (s.chunks + s.shape.groups - 1) / s.shape.groups;
   return s;
 }
 
@@ -309,16 +532,42 @@ NormParams params_of(const gemm_rs_norm_desc* d) {
   return p;
 }
 
+void set_shape(NormParams* p, const Shape& s) {
+  p->warps = s.warps;
+  p->groups = s.groups;
+  p->stages = s.stages;
+}
+
+// Launches Kernel, with more than 48 KB of shared memory allowed once for each device.
+template <auto Kernel, typename... Args>
+int launch(int grid, int threads, int smem, cudaStream_t st, Args... args) {
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return GEMM_RS_ERR_CUDA;
+    }
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  Kernel<<<grid, threads, smem, st>>>(args...);
+  return launch_status();
+}
+
 template <int V>
-void launch_forward(const NormParams& p, int grid, int threads, cudaStream_t st) {
-  norm_forward_kernel<V><<<grid, threads, 0, st>>>(p);
+int launch_forward(const NormParams& p, bool many_gates, int grid, int smem, cudaStream_t st) {
+  const int threads = 32 * p.warps * p.groups;
+  return many_gates ? launch<norm_forward_kernel<V, true>>(grid, threads, smem, st, p)
+                    : launch<norm_forward_kernel<V, false>>(grid, threads, smem, st, p);
 }
 template <int V>
-void launch_backward(const NormParams& p, bool multi, int threads, cudaStream_t st) {
-  if (multi)
-    norm_backward_kernel<V, true><<<p.chunks, threads, 0, st>>>(p);
-  else
-    norm_backward_kernel<V, false><<<p.chunks, threads, 0, st>>>(p);
+int launch_backward(const NormParams& p, GateMode mode, int smem, cudaStream_t st) {
+  const int threads = 32 * p.warps * p.groups;
+  if (mode == kSingle) return launch<norm_backward_kernel<V, kSingle>>(p.blocks, threads, smem, st, p);
+  if (mode == kSequence) return launch<norm_backward_kernel<V, kSequence>>(p.blocks, threads, smem, st, p);
+  return launch<norm_backward_kernel<V, kElement>>(p.blocks, threads, smem, st, p);
 }
 
 const uint4* in(const void* p) { return static_cast<const uint4*>(p); }
@@ -342,24 +591,30 @@ extern "C" int gemm_rs_norm_forward(const gemm_rs_norm_desc* d, const void* x, c
   NormParams p = params_of(d);
   p.x = in(x); p.y = in(y); p.gate = in(gate); p.w_post = in(w_post); p.w_pre = in(w_pre);
   p.r = outp(r); p.h = outp(h); p.stats = static_cast<float*>(stats);
-  const int v = vectors_per_thread(p.nv), threads = threads_for(p.nv, v);
-  const int grid = (int)(p.M < 4ll * sms ? p.M : 4ll * sms);
+  const bool many_gates = d->gate_rows > 1;
+  const int arrays = many_gates ? 3 : 2;
+  Shape s = shape_of(p.nv, arrays, p.M, 2 * sms, kMaxSmem / 2, 0);
+  const int per_sm = forward_blocks(s.v);
+  if (per_sm == 1) s = shape_of(p.nv, arrays, p.M, sms, kMaxSmem, 0);
+  set_shape(&p, s);
+  const long long blocks = (p.M + s.groups - 1) / s.groups;
+  const int grid = (int)(blocks < (long long)per_sm * sms ? blocks : (long long)per_sm * sms);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  switch (v) {
-    case 1: launch_forward<1>(p, grid, threads, st); break;
-    case 2: launch_forward<2>(p, grid, threads, st); break;
-    case 3: launch_forward<3>(p, grid, threads, st); break;
-    default: launch_forward<4>(p, grid, threads, st); break;
+  switch (s.v) {
+    case 1: return launch_forward<1>(p, many_gates, grid, s.smem, st);
+    case 2: return launch_forward<2>(p, many_gates, grid, s.smem, st);
+    case 3: return launch_forward<3>(p, many_gates, grid, s.smem, st);
+    default: return launch_forward<4>(p, many_gates, grid, s.smem, st);
   }
-  return launch_status();
 }
 
 extern "C" int gemm_rs_norm_workspace(const gemm_rs_norm_desc* d, size_t* bytes) {
   const int rc = check(d);
   if (rc) return rc;
   if (!bytes) return GEMM_RS_ERR_INVALID_ARG;
-  // part_pre, part_s or part_post, and two gate slots a chunk
-  const size_t rows = (size_t)split_of(d).chunks * (d->gate_rows > 1 ? 4 : 2);
+  // the blocks' sums for dw_pre and dw_post, and two gate slots a chunk
+  const Split sp = split_of(d);
+  const size_t rows = 2 * (size_t)sp.blocks + (mode_of(d) == kSequence ? 2 * (size_t)sp.chunks : 0);
   *bytes = (rows > 0 ? rows : 1) * (size_t)d->D * sizeof(float);
   return GEMM_RS_OK;
 }
@@ -401,22 +656,34 @@ extern "C" int gemm_rs_norm_backward(const gemm_rs_norm_desc* d, const void* dr,
   p.dx = outp(dx); p.dy = outp(dy); p.dgate = outp(dgate); p.dw_post = outp(dw_post); p.dw_pre = outp(dw_pre);
   p.chunk_rows = sp.chunk_rows;
   p.chunks = sp.chunks;
-  const bool multi = d->gate_rows > 1;
-  float* ws = static_cast<float*>(workspace);
-  const long long plane = (long long)sp.chunks * d->D;
-  p.part_pre = ws;
-  (multi ? p.part_post : p.part_s) = ws + plane;
-  p.part_gate = ws + 2 * plane;
-  const int v = vectors_per_thread(p.nv), threads = threads_for(p.nv, v);
-  switch (v) {
-    case 1: launch_backward<1>(p, multi, threads, st); break;
-    case 2: launch_backward<2>(p, multi, threads, st); break;
-    case 3: launch_backward<3>(p, multi, threads, st); break;
-    default: launch_backward<4>(p, multi, threads, st); break;
+  p.blocks = sp.blocks;
+  set_shape(&p, sp.shape);
+  const GateMode mode = mode_of(d);
+  const long long plane = (long long)sp.blocks * d->D;
+  p.part_pre = static_cast<float*>(workspace);
+  p.part_post = p.part_pre + plane;
+  p.part_gate = p.part_post + plane;
+  switch (sp.shape.v) {
+    case 1: rc = launch_backward<1>(p, mode, sp.shape.smem, st); break;
+    case 2: rc = launch_backward<2>(p, mode, sp.shape.smem, st); break;
+    case 3: rc = launch_backward<3>(p, mode, sp.shape.smem, st); break;
+    default: rc = launch_backward<4>(p, mode, sp.shape.smem, st); break;
   }
-  rc = launch_status();
   if (rc) return rc;
-  const dim3 grid((unsigned)((p.D + 31) / 32), (unsigned)(2 + (multi ? sp.chunks - 1 : 0)));
-  norm_join_kernel<<<grid, 256, 0, st>>>(p, multi ? 1 : 0);
-  return launch_status();
+  const int many_gates = mode != kSingle, by_gate = d->gate_rows < sp.chunks;
+  const long long crossing = mode != kSequence ? 0 : by_gate ? d->gate_rows : sp.chunks - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.D + 31) / 32), (unsigned)(2 + crossing));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];  // its blocks start while the last rows are worked on, and wait
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, norm_join_kernel, (const NormParams&)p, many_gates, by_gate) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_RS_ERR_CUDA;
+  }
+  return GEMM_RS_OK;
 }
