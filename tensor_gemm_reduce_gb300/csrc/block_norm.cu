@@ -63,10 +63,10 @@ Shape shape_of(int nv, int arrays, long long rows, int blocks, int budget, int e
 enum GateMode : int { kSingle = 0, kSequence = 1, kElement = 2 };
 
 struct NormParams {
-  long long M;
+  uint32_t M;               // M * nv stays below 2^32: vector indexes are 32-bit
   int D, nv;                // nv = D / 8 vectors of 16 bytes in a row
   int warps, groups, stages;
-  long long rows_per_gate;  // M / gate_rows
+  uint32_t rows_per_gate;   // M / gate_rows
   float scale, eps, inv_d;
   const uint4 *x, *y, *gate, *w_post, *w_pre;
   uint4 *r, *h;
@@ -74,7 +74,7 @@ struct NormParams {
   // backward
   const uint4 *dr, *dh;
   uint4 *dx, *dy, *dgate, *dw_post, *dw_pre;
-  long long chunk_rows;  // consecutive rows of a group
+  uint32_t chunk_rows;  // consecutive rows of a group
   int chunks, blocks;
   float *part_post, *part_pre, *part_gate;
 };
@@ -98,6 +98,62 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
+}
+
+// Two fp32 values in a register pair: one instruction for both (the kernels are
+// bound by instruction issue as much as by HBM).
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 floats(F2 a) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(a.v));
+  return f;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 both(float a) { return f2(a, a); }
+__device__ __forceinline__ float sum(F2 a) {
+  const float2 f = floats(a);
+  return f.x + f.y;
+}
+__device__ __forceinline__ F2 from_bf16x2(uint32_t w) { return f2(bf16lo_to_f32(w), bf16hi_to_f32(w)); }
+__device__ __forceinline__ uint32_t to_bf16x2(F2 a) {
+  const float2 f = floats(a);
+  return pack_bf16x2(f.x, f.y);
+}
+__device__ __forceinline__ void unpack8(const uint4& v, F2 (&f)[4]) {
+  f[0] = from_bf16x2(v.x);
+  f[1] = from_bf16x2(v.y);
+  f[2] = from_bf16x2(v.z);
+  f[3] = from_bf16x2(v.w);
+}
+__device__ __forceinline__ uint4 pack8(const F2 (&f)[4]) {
+  return make_uint4(to_bf16x2(f[0]), to_bf16x2(f[1]), to_bf16x2(f[2]), to_bf16x2(f[3]));
+}
+__device__ __forceinline__ void store8(float* p, const F2 (&f)[4]) {
+  float4* q = reinterpret_cast<float4*>(p);
+  const float2 a = floats(f[0]), b = floats(f[1]), c = floats(f[2]), d = floats(f[3]);
+  q[0] = make_float4(a.x, a.y, b.x, b.y);
+  q[1] = make_float4(c.x, c.y, d.x, d.y);
 }
 
 // Sums over a group, in each of its threads.  `part` holds kMaxWarps * N
@@ -130,7 +186,10 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* part, int warps,
 // thread 64 registers are enough.
 constexpr int forward_blocks(int v) { return v <= 2 ? 2 : 1; }
 
-// Both sums are over the group, the row stays in registers.
+// The row stays in the ring until it is written: it is unpacked again for each
+// of the two sums and for the outputs.  Keeping it in registers instead spilled
+// some of them, and with most of the SM's memory given to the ring every spill
+// went to L2.
 template <int V, bool kManyGates>
 __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_kernel(const NormParams p) {
   extern __shared__ uint4 ring[];
@@ -140,29 +199,27 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
   const int t = threadIdx.x - group * T;
   const uint32_t mine = smem_u32(ring) + 16u * (group * p.nv + t);
   const uint32_t plane = 16u * p.groups * p.nv;  // one array of a stage
-  const long long step = (long long)gridDim.x * p.groups;
-  long long m = (long long)blockIdx.x * p.groups + group;
+  const uint32_t step = gridDim.x * p.groups;
+  uint32_t m = blockIdx.x * p.groups + group;
   griddep_wait();
 
-  auto fetch = [&](long long row, int stage) {
+  auto fetch = [&](uint32_t row, int stage) {
     if (row < p.M) {
       const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
-      const uint4* gr = kManyGates ? p.gate + (row / p.rows_per_gate) * p.nv : nullptr;
+      const uint32_t at = row * p.nv + t, gat = kManyGates ? row / p.rows_per_gate * p.nv + t : 0;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int i = t + v * T;
-        if (i < p.nv) {
-          cp_async16(base + 16u * v * T, p.y + row * p.nv + i);
-          cp_async16(base + plane + 16u * v * T, p.x + row * p.nv + i);
-          if (kManyGates) cp_async16(base + 2 * plane + 16u * v * T, gr + i);
+      for (int v = 0; v < V; ++v)
+        if (t + v * T < p.nv) {
+          cp_async16(base + 16u * v * T, p.y + (at + v * T));
+          cp_async16(base + plane + 16u * v * T, p.x + (at + v * T));
+          if (kManyGates) cp_async16(base + 2 * plane + 16u * v * T, p.gate + (gat + v * T));
         }
-      }
     }
     cp_async_commit();
   };
   for (int s = 0; s < p.stages; ++s) fetch(m + s * step, s);
   // w_post, times scale and the gate when there is one row of it
-  float gw[V][8];
+  F2 gw[V][4];
   uint4 wq[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -170,60 +227,74 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
     if (i < p.nv) {
       unpack8(__ldg(p.w_post + i), gw[v]);
       wq[v] = __ldg(p.w_pre + i);
-      float g[8];
-      if (!kManyGates && p.gate) unpack8(__ldg(p.gate + i), g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) gw[v][j] *= !kManyGates && p.gate ? p.scale * g[j] : p.scale;
+      for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * both(p.scale);
+      if (!kManyGates && p.gate) {
+        F2 g[4];
+        unpack8(__ldg(p.gate + i), g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * g[j];
+      }
     }
   }
 
   int stage = 0;
+#pragma unroll 1
   for (; m < p.M; m += step) {
     cp_async_wait(p.stages);
     const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
-    float r[V][8];
-    float s[1] = {0.f};
+    F2 s2 = both(0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (t + v * T < p.nv) {
-        float y[8];
+        F2 y[4];
         unpack8(ld_shared_v4(base + 16u * v * T), y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] = fmaf(y[j], y[j], s[0]);
+        for (int j = 0; j < 4; ++j) s2 = fma2(y[j], y[j], s2);
       }
+    float s[1] = {sum(s2)};
     group_sum<1>(s, part[group][0], p.warps, group);
     const float pn = 1.f / sqrtf(fmaf(s[0], p.inv_d, p.eps));
-    s[0] = 0.f;
+    const F2 pn2 = both(pn);
+    // r of one vector, from the ring
+    auto residual = [&](int v, F2 (&r)[4]) {
+      F2 y[4], g[4];
+      unpack8(ld_shared_v4(base + 16u * v * T), y);
+      unpack8(ld_shared_v4(base + plane + 16u * v * T), r);
+      if (kManyGates) unpack8(ld_shared_v4(base + 2 * plane + 16u * v * T), g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const F2 yn = y[j] * pn2;
+        r[j] = kManyGates ? fma2(g[j], yn * gw[v][j], r[j]) : fma2(yn, gw[v][j], r[j]);
+      }
+    };
+    s2 = both(0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (t + v * T < p.nv) {
-        float y[8], g[8];
-        unpack8(ld_shared_v4(base + 16u * v * T), y);
-        unpack8(ld_shared_v4(base + plane + 16u * v * T), r[v]);
-        if (kManyGates) unpack8(ld_shared_v4(base + 2 * plane + 16u * v * T), g);
+        F2 r[4];
+        residual(v, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float u = y[j] * pn * gw[v][j];
-          r[v][j] = kManyGates ? fmaf(g[j], u, r[v][j]) : r[v][j] + u;
-          s[0] = fmaf(r[v][j], r[v][j], s[0]);
-        }
+        for (int j = 0; j < 4; ++j) s2 = fma2(r[j], r[j], s2);
       }
-    fetch(m + p.stages * step, stage);  // the row is in registers: its slot is free
-    if (++stage == p.stages) stage = 0;
+    s[0] = sum(s2);
     group_sum<1>(s, part[group][1], p.warps, group);
     const float qn = 1.f / sqrtf(fmaf(s[0], p.inv_d, p.eps));
+    const F2 qn2 = both(qn);
+    const uint32_t at = m * p.nv + t;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int i = t + v * T;
-      if (i < p.nv) {
-        float w[8], h[8];
+    for (int v = 0; v < V; ++v)
+      if (t + v * T < p.nv) {
+        F2 r[4], w[4];
+        residual(v, r);
+        p.r[at + v * T] = pack8(r);
         unpack8(wq[v], w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = r[v][j] * qn * w[j];
-        p.r[m * p.nv + i] = pack8(r[v]);
-        p.h[m * p.nv + i] = pack8(h);
+        for (int j = 0; j < 4; ++j) w[j] = w[j] * (r[j] * qn2);
+        p.h[at + v * T] = pack8(w);
       }
-    }
+    fetch(m + p.stages * step, stage);  // every read of the slot is done
+    if (++stage == p.stages) stage = 0;
     if (p.stats && t == 0) {
       p.stats[m] = pn;
       p.stats[p.M + m] = qn;
@@ -238,7 +309,7 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
 //                                                    = mean(c (dr + q a)) - q m1 mean(c rn)
 // so one sum of three values over the row serves both norms.
 // Each group owns chunk_rows consecutive rows and its threads own columns, so
-// the sums over rows stay in registers: the sum of t yn over the rows of one
+// the sums over rows stay in registers: the sum S of t yn over the rows of one
 // gate row gives both dgate = scale w_post S and that gate row's share
 // scale gate S of dw_post; the sum of dh rn is dw_pre.  kSequence adds the
 // shares of dw_post in shared memory, at the end of each gate row; kElement
@@ -246,6 +317,7 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
 // one that crosses a chunk border leaves a partial sum in slot 2 c (its rows
 // begin at the chunk's first row or before) or 2 c + 1.  At the end the
 // block's groups are added and the block writes one row of partial sums.
+// As in the forward pass the row is unpacked twice rather than kept.
 template <int V, int kMode>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const NormParams p) {
   extern __shared__ uint4 ring[];
@@ -257,137 +329,157 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   const uint32_t plane = 16u * p.groups * p.nv;
   // kSequence: this thread's columns of dw_post, after the ring
   float* post = reinterpret_cast<float*>(ring + (size_t)p.stages * kArrays * p.groups * p.nv) + 8 * (group * p.nv + t);
-  const long long c = (long long)blockIdx.x * p.groups + group;
-  const long long m0 = c * p.chunk_rows;
-  const long long m1 = m0 + p.chunk_rows < p.M ? m0 + p.chunk_rows : p.M;
+  const uint32_t c = blockIdx.x * p.groups + group;
+  const uint32_t m0 = c * p.chunk_rows < p.M ? c * p.chunk_rows : p.M;
+  const uint32_t m1 = m0 + p.chunk_rows < p.M ? m0 + p.chunk_rows : p.M;
   griddep_wait();
 
-  auto fetch = [&](long long row, int stage) {
+  auto fetch = [&](uint32_t row, int stage) {
     if (row < m1) {
       const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
-      const uint4* gr = kMode != kSingle ? p.gate + (row / p.rows_per_gate) * p.nv : nullptr;
+      const uint32_t at = row * p.nv + t;
+      const uint32_t gat = kMode == kSequence ? row / p.rows_per_gate * p.nv + t : at;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int i = t + v * T;
-        if (i < p.nv) {
+      for (int v = 0; v < V; ++v)
+        if (t + v * T < p.nv) {
           const uint32_t dst = base + 16u * v * T;
-          cp_async16(dst, p.y + row * p.nv + i);
-          cp_async16(dst + plane, p.x + row * p.nv + i);
-          cp_async16(dst + 2 * plane, p.dr + row * p.nv + i);
-          cp_async16(dst + 3 * plane, p.dh + row * p.nv + i);
-          if (kMode != kSingle) cp_async16(dst + 4 * plane, gr + i);
+          cp_async16(dst, p.y + (at + v * T));
+          cp_async16(dst + plane, p.x + (at + v * T));
+          cp_async16(dst + 2 * plane, p.dr + (at + v * T));
+          cp_async16(dst + 3 * plane, p.dh + (at + v * T));
+          if (kMode != kSingle) cp_async16(dst + 4 * plane, p.gate + (gat + v * T));
         }
-      }
     }
     cp_async_commit();
   };
   for (int s = 0; s < p.stages; ++s) fetch(m0 + s, s);
 
-  float gw[V][8];  // scale w_post, times the gate when there is one row of it
+  F2 gw[V][4];  // scale w_post, times the gate when there is one row of it
   uint4 wq[V];
-  float S[V][8], Ppre[V][8];  // kElement: S is this thread's sum for dw_post
+  F2 S[V][4], Ppre[V][4];  // kElement: S is this thread's sum for dw_post
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int i = t + v * T;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) S[v][j] = Ppre[v][j] = 0.f;
+    for (int j = 0; j < 4; ++j) S[v][j] = Ppre[v][j] = both(0.f);
     if (i < p.nv) {
       unpack8(__ldg(p.w_post + i), gw[v]);
       wq[v] = __ldg(p.w_pre + i);
-      float g[8];
-      if (kMode == kSingle && p.gate) unpack8(__ldg(p.gate + i), g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        gw[v][j] *= kMode == kSingle && p.gate ? p.scale * g[j] : p.scale;
-        if (kMode == kSequence) post[8 * v * T + j] = 0.f;
+      for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * both(p.scale);
+      if (kMode == kSingle && p.gate) {
+        F2 g[4];
+        unpack8(__ldg(p.gate + i), g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * g[j];
       }
+      if (kMode == kSequence) store8(post + 8 * v * T, S[v]);
     }
   }
 
   int stage = 0;
-  for (long long m = m0; m < m1; ++m) {
-    const float pn = __ldg(p.stats + m), qn = __ldg(p.stats + p.M + m);
+  // the rows' statistics, one row ahead
+  float pn_next = m0 < m1 ? __ldg(p.stats + m0) : 0.f, qn_next = m0 < m1 ? __ldg(p.stats + p.M + m0) : 0.f;
+#pragma unroll 1
+  for (uint32_t m = m0; m < m1; ++m) {
+    const float pn = pn_next, qn = qn_next;
+    if (m + 1 < m1) {
+      pn_next = __ldg(p.stats + m + 1);
+      qn_next = __ldg(p.stats + p.M + m + 1);
+    }
     cp_async_wait(p.stages);
     const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
-    float yn[V][8], rn[V][8], z[V][8];  // z = dr + q a
-    uint4 gp[V];                        // this row's gate
-    float s[3] = {0.f, 0.f, 0.f};
+    F2 s0 = both(0.f), s1 = s0, s2 = s0;
+    const F2 pn2 = both(pn), qn2 = both(qn);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (t + v * T < p.nv) {
         const uint32_t src = base + 16u * v * T;
-        float x[8], g[8], dh[8], w[8];
-        unpack8(ld_shared_v4(src), yn[v]);
+        F2 y[4], x[4], z[4], dh[4], w[4], g[4];
+        unpack8(ld_shared_v4(src), y);
         unpack8(ld_shared_v4(src + plane), x);
-        unpack8(ld_shared_v4(src + 2 * plane), z[v]);
+        unpack8(ld_shared_v4(src + 2 * plane), z);
         unpack8(ld_shared_v4(src + 3 * plane), dh);
         unpack8(wq[v], w);
-        if (kMode != kSingle) {
-          gp[v] = ld_shared_v4(src + 4 * plane);
-          unpack8(gp[v], g);
-        }
+        if (kMode != kSingle) unpack8(ld_shared_v4(src + 4 * plane), g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          yn[v][j] *= pn;
-          const float br = (kMode != kSingle ? g[j] * gw[v][j] : gw[v][j]) * yn[v][j];
-          rn[v][j] = (x[j] + br) * qn;
-          const float a = dh[j] * w[j];
-          z[v][j] = fmaf(qn, a, z[v][j]);
-          Ppre[v][j] = fmaf(dh[j], rn[v][j], Ppre[v][j]);
-          s[0] = fmaf(a, rn[v][j], s[0]);
-          s[1] = fmaf(br, z[v][j], s[1]);
-          s[2] = fmaf(br, rn[v][j], s[2]);
+        for (int j = 0; j < 4; ++j) {
+          const F2 br = (kMode != kSingle ? g[j] * gw[v][j] : gw[v][j]) * (y[j] * pn2);
+          const F2 rn = (x[j] + br) * qn2;
+          const F2 a = dh[j] * w[j];
+          Ppre[v][j] = fma2(dh[j], rn, Ppre[v][j]);
+          s0 = fma2(a, rn, s0);
+          s1 = fma2(br, fma2(qn2, a, z[j]), s1);
+          s2 = fma2(br, rn, s2);
         }
       }
     }
-    fetch(m + p.stages, stage);  // the row is in registers: its slot is free
-    if (++stage == p.stages) stage = 0;
+    float s[3] = {sum(s0), sum(s1), sum(s2)};
     group_sum<3>(s, part[group][m & 1], p.warps, group);
     const float k1 = qn * (s[0] * p.inv_d);                 // q m1
     const float k2 = fmaf(-k1, s[2], s[1]) * p.inv_d * pn;  // p m2
-    const long long gi = kMode == kSequence ? m / p.rows_per_gate : m;
-    const bool last = kMode == kSequence && (m + 1 == m1 || (m + 1) % p.rows_per_gate == 0);
+    const F2 nk1 = both(-k1), nk2 = both(-k2);
+    const uint32_t gi = kMode == kSequence ? m / p.rows_per_gate : m;
+    const bool last = kMode == kSequence && (m + 1 == m1 || m + 1 == (gi + 1) * p.rows_per_gate);
+    const uint32_t at = m * p.nv + t;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int i = t + v * T;
-      if (i < p.nv) {
-        float g[8], dx[8], dy[8], dg[8];
-        if (kMode != kSingle) unpack8(gp[v], g);
+      if (t + v * T < p.nv) {
+        const uint32_t src = base + 16u * v * T;
+        F2 yn[4], g[4], dx[4], dy[4];
+        {
+          F2 x[4], dh[4], w[4];
+          unpack8(ld_shared_v4(src), yn);
+          unpack8(ld_shared_v4(src + plane), x);
+          unpack8(ld_shared_v4(src + 2 * plane), dx);
+          unpack8(ld_shared_v4(src + 3 * plane), dh);
+          unpack8(wq[v], w);
+          if (kMode != kSingle) unpack8(ld_shared_v4(src + 4 * plane), g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float tt = fmaf(-k1, rn[v][j], z[v][j]);
-          const float ty = tt * yn[v][j];
-          dx[j] = tt;
-          dy[j] = fmaf(pn * tt, kMode != kSingle ? g[j] * gw[v][j] : gw[v][j], -k2 * yn[v][j]);
-          if (kMode == kElement) {
-            dg[j] = gw[v][j] * ty;
-            S[v][j] = fmaf(g[j], ty, S[v][j]);
-          } else {
-            S[v][j] += ty;
+          for (int j = 0; j < 4; ++j) {
+            yn[j] = yn[j] * pn2;
+            const F2 f = kMode != kSingle ? g[j] * gw[v][j] : gw[v][j];
+            const F2 e = fma2(nk1, fma2(f, yn[j], x[j]), dh[j] * w[j]);  // a - rn m1
+            dx[j] = fma2(qn2, e, dx[j]);
+            dy[j] = fma2(dx[j] * f, pn2, nk2 * yn[j]);
           }
         }
-        p.dx[m * p.nv + i] = pack8(dx);
-        p.dy[m * p.nv + i] = pack8(dy);
-        if (kMode == kElement) p.dgate[m * p.nv + i] = pack8(dg);
+        p.dx[at + v * T] = pack8(dx);
+        p.dy[at + v * T] = pack8(dy);
+        if (kMode == kElement) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const F2 ty = dx[j] * yn[j];
+            S[v][j] = fma2(g[j], ty, S[v][j]);
+            dx[j] = gw[v][j] * ty;
+          }
+          p.dgate[at + v * T] = pack8(dx);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) S[v][j] = fma2(dx[j], yn[j], S[v][j]);
+        }
         if (kMode == kSequence && last) {  // end of a gate row's rows in this chunk
-          const long long first = gi * p.rows_per_gate;
+          const uint32_t first = gi * p.rows_per_gate;
+          const int i = t + v * T;
           if (first >= m0 && first + p.rows_per_gate <= m1) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dg[j] = gw[v][j] * S[v][j];
-            p.dgate[gi * p.nv + i] = pack8(dg);
+            for (int j = 0; j < 4; ++j) dx[j] = gw[v][j] * S[v][j];
+            p.dgate[gi * p.nv + i] = pack8(dx);
           } else {
-            float* slot = p.part_gate + (2 * c + (first > m0 ? 1 : 0)) * (long long)p.D + 8 * i;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) slot[j] = S[v][j];
+            store8(p.part_gate + (2ll * c + (first > m0 ? 1 : 0)) * p.D + 8 * i, S[v]);
           }
+          float* mp = post + 8 * v * T;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            post[8 * v * T + j] = fmaf(g[j], S[v][j], post[8 * v * T + j]);
-            S[v][j] = 0.f;
+          for (int j = 0; j < 4; ++j) {
+            dy[j] = fma2(g[j], S[v][j], f2(mp[2 * j], mp[2 * j + 1]));
+            S[v][j] = both(0.f);
           }
+          store8(mp, dy);
         }
       }
     }
+    fetch(m + p.stages, stage);  // every read of the slot is done
+    if (++stage == p.stages) stage = 0;
   }
   griddep_launch_dependents();
 
@@ -397,31 +489,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
     for (int v = 0; v < V; ++v)
       if (t + v * T < p.nv)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) S[v][j] = post[8 * v * T + j];
+        for (int j = 0; j < 4; ++j) S[v][j] = f2(post[8 * v * T + 2 * j], post[8 * v * T + 2 * j + 1]);
   float* sums = reinterpret_cast<float*>(ring);
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     float* out = (which ? p.part_pre : p.part_post) + (long long)blockIdx.x * p.D;
-    if (p.groups == 1) {
+    if (p.groups > 1) __syncthreads();
+    float* to = p.groups > 1 ? sums + group * p.D : out;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int i = t + v * T;
-        if (i < p.nv) {
-          const float(&f)[8] = which ? Ppre[v] : S[v];
-          reinterpret_cast<float4*>(out)[2 * i] = make_float4(f[0], f[1], f[2], f[3]);
-          reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
-        }
-      }
-      continue;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int i = t + v * T;
-      if (i < p.nv)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sums[group * p.D + 8 * i + j] = which ? Ppre[v][j] : S[v][j];
-    }
+    for (int v = 0; v < V; ++v)
+      if (t + v * T < p.nv) store8(to + 8 * (t + v * T), which ? Ppre[v] : S[v]);
+    if (p.groups == 1) continue;
     __syncthreads();
     for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
       float f = 0.f;
@@ -452,7 +530,7 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const NormParams p, int 
   } else if (job == 1) {
     src = p.part_post;
   } else {
-    gi = by_gate ? job - 2 : (job - 1) * p.chunk_rows / p.rows_per_gate;
+    gi = by_gate ? job - 2 : (long long)(job - 1) * p.chunk_rows / p.rows_per_gate;
     const long long first = gi * p.rows_per_gate, last = first + p.rows_per_gate - 1;
     const long long b = first / p.chunk_rows;
     if (last / p.chunk_rows == b || (!by_gate && b != job - 2)) return;
@@ -491,7 +569,7 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const NormParams p, int 
 int check(const gemm_rs_norm_desc* d) {
   if (!d || d->gate_rows < 0 || !(d->eps >= 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->scale))
     return GEMM_RS_ERR_INVALID_ARG;
-  if (d->M < 0 || d->M > (1ll << 40) || d->D <= 0 || d->D % 8 || d->D > GEMM_RS_NORM_MAX_D)
+  if (d->M < 0 || d->D <= 0 || d->D % 8 || d->D > GEMM_RS_NORM_MAX_D || d->M >= (1ll << 35) / d->D)
     return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
   if (d->gate_rows > 0 && (d->M % d->gate_rows || (d->M > 0 && d->gate_rows > d->M)))
     return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
@@ -522,10 +600,10 @@ Split split_of(const gemm_rs_norm_desc* d) {
 
 NormParams params_of(const gemm_rs_norm_desc* d) {
   NormParams p = {};
-  p.M = d->M;
+  p.M = (uint32_t)d->M;
   p.D = (int)d->D;
   p.nv = (int)(d->D / 8);
-  p.rows_per_gate = d->gate_rows > 0 && d->M > 0 ? d->M / d->gate_rows : 1;
+  p.rows_per_gate = d->gate_rows > 0 && d->M > 0 ? (uint32_t)(d->M / d->gate_rows) : 1;
   p.scale = d->scale;
   p.eps = d->eps;
   p.inv_d = 1.f / (float)d->D;
@@ -593,11 +671,11 @@ extern "C" int gemm_rs_norm_forward(const gemm_rs_norm_desc* d, const void* x, c
   p.r = outp(r); p.h = outp(h); p.stats = static_cast<float*>(stats);
   const bool many_gates = d->gate_rows > 1;
   const int arrays = many_gates ? 3 : 2;
-  Shape s = shape_of(p.nv, arrays, p.M, 2 * sms, kMaxSmem / 2, 0);
+  Shape s = shape_of(p.nv, arrays, d->M, 2 * sms, kMaxSmem / 2, 0);
   const int per_sm = forward_blocks(s.v);
-  if (per_sm == 1) s = shape_of(p.nv, arrays, p.M, sms, kMaxSmem, 0);
+  if (per_sm == 1) s = shape_of(p.nv, arrays, d->M, sms, kMaxSmem, 0);
   set_shape(&p, s);
-  const long long blocks = (p.M + s.groups - 1) / s.groups;
+  const long long blocks = (d->M + s.groups - 1) / s.groups;
   const int grid = (int)(blocks < (long long)per_sm * sms ? blocks : (long long)per_sm * sms);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (s.v) {
@@ -654,7 +732,7 @@ extern "C" int gemm_rs_norm_backward(const gemm_rs_norm_desc* d, const void* dr,
   p.dr = in(dr); p.dh = in(dh);
   p.stats = static_cast<float*>(const_cast<void*>(stats));
   p.dx = outp(dx); p.dy = outp(dy); p.dgate = outp(dgate); p.dw_post = outp(dw_post); p.dw_pre = outp(dw_pre);
-  p.chunk_rows = sp.chunk_rows;
+  p.chunk_rows = (uint32_t)sp.chunk_rows;
   p.chunks = sp.chunks;
   p.blocks = sp.blocks;
   set_shape(&p, sp.shape);
