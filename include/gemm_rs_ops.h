@@ -41,7 +41,7 @@ extern "C" {
  * from the unrounded r.
  */
 typedef struct gemm_rs_norm_desc {
-  int64_t M, D;       /* M >= 0; D a positive multiple of 8, at most 16384; M * D < 2^35 */
+  int64_t M, D;       /* M >= 0; D a positive multiple of 8, at most 16384; M * D <= 2^34 */
   int64_t gate_rows;  /* 0: no gate; else a positive divisor of M (any, if M = 0) */
   float scale;        /* residual scale of the block's branch */
   float eps;          /* >= 0; not read by the backward pass */

@@ -12,7 +12,8 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 constexpr int kMaxWarps = kMaxThreads / 32;
-constexpr int kMaxSmem = 200 * 1024;  // of 227 KB; the rest stays L1 for the weights
+constexpr int kMaxSmem = 224 * 1024;  // of the SM's 228 KB
+constexpr int kBackwardSmem = 200 * 1024;
 // The backward pass cuts the rows into at most kBlocks x groups chunks, one
 // block per SM of a GB300.  A constant, so that the workspace size and the
 // order of the sums do not depend on the device.
@@ -51,7 +52,9 @@ Shape shape_of(int nv, int arrays, long long rows, int blocks, int budget, int e
   const int row = s.groups * nv * 16;
   const int extra = s.groups * nv * extra_per_vector;
   s.stages = (budget - extra) / (arrays * row);
-  if (s.stages > 4) s.stages = 4;
+  // Two are enough: a third row in flight gained nothing on 8192 rows of 8192
+  // and queued in front of the first row on 1003 (16.5 against 15.2 us).
+  if (s.stages > 2) s.stages = 2;
   if (s.stages < 1) s.stages = 1;
   s.smem = s.stages * arrays * row + extra;
   return s;
@@ -63,7 +66,7 @@ Shape shape_of(int nv, int arrays, long long rows, int blocks, int budget, int e
 enum GateMode : int { kSingle = 0, kSequence = 1, kElement = 2 };
 
 struct NormParams {
-  uint32_t M;               // M * nv stays below 2^32: vector indexes are 32-bit
+  uint32_t M;               // M * nv stays below 2^31: vector indexes are 32-bit
   int D, nv;                // nv = D / 8 vectors of 16 bytes in a row
   int warps, groups, stages;
   uint32_t rows_per_gate;   // M / gate_rows
@@ -74,7 +77,11 @@ struct NormParams {
   // backward
   const uint4 *dr, *dh;
   uint4 *dx, *dy, *dgate, *dw_post, *dw_pre;
-  uint32_t chunk_rows;  // consecutive rows of a group
+  // Rows of a group: chunk_rows consecutive ones (step = 1) where a gate row
+  // serves several of them, else rows `step` = the number of groups apart, so
+  // that all blocks work on one region of memory at a time (8192 x 8192: 101 ->
+  // 96 us forward, 133 -> 127 us backward).
+  uint32_t chunk_rows, step;
   int chunks, blocks;
   float *part_post, *part_pre, *part_gate;
 };
@@ -85,11 +92,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Wait until at most `stages` - 1 of this thread's copy groups are pending.
 __device__ __forceinline__ void cp_async_wait(int stages) {
-  if (stages >= 4)
-    asm volatile("cp.async.wait_group 3;" ::: "memory");
-  else if (stages == 3)
-    asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else if (stages == 2)
+  if (stages == 2)
     asm volatile("cp.async.wait_group 1;" ::: "memory");
   else
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -156,142 +159,174 @@ __device__ __forceinline__ void store8(float* p, const F2 (&f)[4]) {
   q[1] = make_float4(c.x, c.y, d.x, d.y);
 }
 
-// Sums over a group, in each of its threads.  `part` holds kMaxWarps * N
-// floats of this group; a group alternates between two of them, so that one
+// Sums of four values over a group, in each of its threads.  The first two
+// exchanges halve the values that a lane carries (lane bits 4 and 3 select one
+// of the four), so a warp takes 6 shuffles instead of 20.  `part` has a place
+// for each value and warp; a group alternates between two of them, so that one
 // barrier a sum is enough.
-template <int N>
-__device__ __forceinline__ void group_sum(float (&v)[N], float* part, int warps, int group) {
+__device__ __forceinline__ void group_sum4(float (&v)[4], float (&part)[4][kMaxWarps], int warps, int group) {
+  const int lane = threadIdx.x & 31;
+  const bool hi = lane & 16, odd = lane & 8;
+  const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+  const float b = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
+  float s = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  // lanes 8 i .. 8 i + 7 hold the warp's sum of value i
+  if (warps > 1) {
+    if ((lane & 7) == 0) part[lane >> 3][threadIdx.x >> 5] = s;
+    asm volatile("barrier.sync.aligned %0, %1;" ::"r"(group + 1), "r"(32 * warps) : "memory");
+    // lane 8 i + j adds value i of warps j and j + 8
+    const int j = lane & 7;
+    const float* row = &part[lane >> 3][group * warps];
+    s = (j < warps ? row[j] : 0.f) + (j + 8 < warps ? row[j + 8] : 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (warps == 1) return;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - group * warps;
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) part[i * kMaxWarps + warp] = v[i];
-  asm volatile("barrier.sync.aligned %0, %1;" ::"r"(group + 1), "r"(32 * warps) : "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int w = lane % kMaxWarps;  // both halves of the warp add the same values
-    v[i] = w < warps ? part[i * kMaxWarps + w] : 0.f;
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   }
 #pragma unroll
-  for (int o = kMaxWarps / 2; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, s, 8 * i);
 }
 
 // Blocks of the forward kernel that share an SM: with up to two vectors a
 // thread 64 registers are enough.
 constexpr int forward_blocks(int v) { return v <= 2 ? 2 : 1; }
 
-// The row stays in the ring until it is written: it is unpacked again for each
-// of the two sums and for the outputs.  Keeping it in registers instead spilled
-// some of them, and with most of the SM's memory given to the ring every spill
-// went to L2.
-template <int V, bool kManyGates>
+// With c = scale gate w_post y the row's residual is r = x + p c, so
+//   sum r^2 = sum x^2 + 2 p sum x c + p^2 sum c^2
+// and one sum of four values (y^2, x^2, x c, c^2) serves both norms.  Where the
+// branch cancels most of x (the result is under a quarter of the positive
+// terms) the rounding of the terms would show, and sum r^2 is taken directly.
+// The row stays in the ring until it is written and is unpacked twice: keeping
+// it in registers spilled some of them, and with most of the SM's memory given
+// to the ring every spill went to L2.
+// A gate row that serves several consecutive rows of a group stays in registers
+// with w_post; kGateRing: gate rows change too often for
+// that and arrive through the ring.
+template <int V, bool kGateRing>
 __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_kernel(const NormParams p) {
   extern __shared__ uint4 ring[];
-  __shared__ float part[kMaxWarps][2][kMaxWarps];
-  constexpr int kArrays = kManyGates ? 3 : 2;
+  __shared__ float part[2][4][kMaxWarps];
+  constexpr int kArrays = kGateRing ? 3 : 2;
   const int group = (int)(threadIdx.x >> 5) / p.warps, T = 32 * p.warps;
   const int t = threadIdx.x - group * T;
   const uint32_t mine = smem_u32(ring) + 16u * (group * p.nv + t);
   const uint32_t plane = 16u * p.groups * p.nv;  // one array of a stage
-  const uint32_t step = gridDim.x * p.groups;
-  uint32_t m = blockIdx.x * p.groups + group;
+  const uint32_t c = blockIdx.x * p.groups + group, step = p.step;
+  const uint32_t m0 = step == 1 ? c * p.chunk_rows : c;
+  const uint32_t m1 = step == 1 && m0 + p.chunk_rows < p.M ? m0 + p.chunk_rows : p.M;
   griddep_wait();
 
   auto fetch = [&](uint32_t row, int stage) {
-    if (row < p.M) {
+    if (row < m1) {
       const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
-      const uint32_t at = row * p.nv + t, gat = kManyGates ? row / p.rows_per_gate * p.nv + t : 0;
+      const uint32_t at = row * p.nv + t, gat = kGateRing ? row / p.rows_per_gate * p.nv + t : 0;
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (t + v * T < p.nv) {
           cp_async16(base + 16u * v * T, p.y + (at + v * T));
           cp_async16(base + plane + 16u * v * T, p.x + (at + v * T));
-          if (kManyGates) cp_async16(base + 2 * plane + 16u * v * T, p.gate + (gat + v * T));
+          if (kGateRing) cp_async16(base + 2 * plane + 16u * v * T, p.gate + (gat + v * T));
         }
     }
     cp_async_commit();
   };
-  for (int s = 0; s < p.stages; ++s) fetch(m + s * step, s);
-  // w_post, times scale and the gate when there is one row of it
-  F2 gw[V][4];
-  uint4 wq[V];
+  for (int s = 0; s < p.stages; ++s) fetch(m0 + s * step, s);
+  // this thread's vectors of w_pre, after the ring: 64 registers do not hold
+  // them, and L1 has too little room beside the ring
+  uint4* w_pre = ring + (size_t)(p.stages * kArrays) * p.groups * p.nv + group * p.nv + t;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int i = t + v * T;
-    if (i < p.nv) {
-      unpack8(__ldg(p.w_post + i), gw[v]);
-      wq[v] = __ldg(p.w_pre + i);
+  for (int v = 0; v < V; ++v)
+    if (t + v * T < p.nv) w_pre[v * T] = __ldg(p.w_pre + t + v * T);
+  F2 gw[V][4];  // scale w_post, times the gate unless it is in the ring
+  auto branch_weights = [&](uint32_t gate_row) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * both(p.scale);
-      if (!kManyGates && p.gate) {
-        F2 g[4];
-        unpack8(__ldg(p.gate + i), g);
+    for (int v = 0; v < V; ++v)
+      if (t + v * T < p.nv) {
+        unpack8(__ldg(p.w_post + t + v * T), gw[v]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * g[j];
+        for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * both(p.scale);
+        if (!kGateRing && p.gate) {
+          F2 g[4];
+          unpack8(__ldg(p.gate + gate_row * p.nv + t + v * T), g);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * g[j];
+        }
       }
-    }
-  }
+  };
+  uint32_t gate_row = p.gate ? m0 / p.rows_per_gate : 0, gate_end = p.gate ? (gate_row + 1) * p.rows_per_gate : p.M;
+  if (m0 < p.M) branch_weights(gate_row);
 
   int stage = 0;
+  uint32_t it = 0;
 #pragma unroll 1
-  for (; m < p.M; m += step) {
+  for (uint32_t m = m0; m < m1; m += step, ++it) {
+    if (!kGateRing && m == gate_end) {
+      branch_weights(++gate_row);
+      gate_end += p.rows_per_gate;
+    }
     cp_async_wait(p.stages);
     const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
-    F2 s2 = both(0.f);
+    // y, x and the branch c of one vector, from the ring
+    auto load = [&](int v, F2 (&y)[4], F2 (&x)[4], F2 (&c)[4]) {
+      unpack8(ld_shared_v4(base + 16u * v * T), y);
+      unpack8(ld_shared_v4(base + plane + 16u * v * T), x);
+      if (kGateRing) unpack8(ld_shared_v4(base + 2 * plane + 16u * v * T), c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] = kGateRing ? c[j] * gw[v][j] * y[j] : gw[v][j] * y[j];
+    };
+    F2 yy = both(0.f), xx = yy, xc = yy, cc = yy;
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (t + v * T < p.nv) {
-        F2 y[4];
-        unpack8(ld_shared_v4(base + 16u * v * T), y);
+        F2 y[4], x[4], c[4];
+        load(v, y, x, c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s2 = fma2(y[j], y[j], s2);
+        for (int j = 0; j < 4; ++j) {
+          yy = fma2(y[j], y[j], yy);
+          xx = fma2(x[j], x[j], xx);
+          xc = fma2(x[j], c[j], xc);
+          cc = fma2(c[j], c[j], cc);
+        }
       }
-    float s[1] = {sum(s2)};
-    group_sum<1>(s, part[group][0], p.warps, group);
+    float s[4] = {sum(yy), sum(xx), sum(xc), sum(cc)};
+    group_sum4(s, part[it & 1], p.warps, group);
     const float pn = 1.f / sqrtf(fmaf(s[0], p.inv_d, p.eps));
     const F2 pn2 = both(pn);
-    // r of one vector, from the ring
-    auto residual = [&](int v, F2 (&r)[4]) {
-      F2 y[4], g[4];
-      unpack8(ld_shared_v4(base + 16u * v * T), y);
-      unpack8(ld_shared_v4(base + plane + 16u * v * T), r);
-      if (kManyGates) unpack8(ld_shared_v4(base + 2 * plane + 16u * v * T), g);
+    const float terms = fmaf(pn * pn, s[3], s[1]);
+    float rr = fmaf(2.f * pn, s[2], terms);
+    if (!(rr >= 0.25f * terms)) {  // the same in every thread of the group; also for an infinite term
+      F2 acc = both(0.f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const F2 yn = y[j] * pn2;
-        r[j] = kManyGates ? fma2(g[j], yn * gw[v][j], r[j]) : fma2(yn, gw[v][j], r[j]);
-      }
-    };
-    s2 = both(0.f);
+      for (int v = 0; v < V; ++v)
+        if (t + v * T < p.nv) {
+          F2 y[4], x[4], c[4];
+          load(v, y, x, c);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (t + v * T < p.nv) {
-        F2 r[4];
-        residual(v, r);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s2 = fma2(r[j], r[j], s2);
-      }
-    s[0] = sum(s2);
-    group_sum<1>(s, part[group][1], p.warps, group);
-    const float qn = 1.f / sqrtf(fmaf(s[0], p.inv_d, p.eps));
+          for (int j = 0; j < 4; ++j) {
+            const F2 r = fma2(c[j], pn2, x[j]);
+            acc = fma2(r, r, acc);
+          }
+        }
+      float d[4] = {sum(acc), 0.f, 0.f, 0.f};
+      if (p.warps > 1) asm volatile("barrier.sync.aligned %0, %1;" ::"r"(group + 1), "r"(32 * p.warps) : "memory");
+      group_sum4(d, part[it & 1], p.warps, group);
+      rr = d[0];
+    }
+    const float qn = 1.f / sqrtf(fmaf(rr, p.inv_d, p.eps));
     const F2 qn2 = both(qn);
     const uint32_t at = m * p.nv + t;
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (t + v * T < p.nv) {
-        F2 r[4], w[4];
-        residual(v, r);
-        p.r[at + v * T] = pack8(r);
-        unpack8(wq[v], w);
+        F2 y[4], x[4], c[4];
+        load(v, y, x, c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = w[j] * (r[j] * qn2);
-        p.h[at + v * T] = pack8(w);
+        for (int j = 0; j < 4; ++j) x[j] = fma2(c[j], pn2, x[j]);
+        p.r[at + v * T] = pack8(x);
+        unpack8(w_pre[v * T], y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = y[j] * (x[j] * qn2);
+        p.h[at + v * T] = pack8(x);
       }
     fetch(m + p.stages * step, stage);  // every read of the slot is done
     if (++stage == p.stages) stage = 0;
@@ -308,8 +343,8 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
 //   dy = p (scale gate t w_post - yn m2),         m2 = mean(scale gate t w_post yn)
 //                                                    = mean(c (dr + q a)) - q m1 mean(c rn)
 // so one sum of three values over the row serves both norms.
-// Each group owns chunk_rows consecutive rows and its threads own columns, so
-// the sums over rows stay in registers: the sum S of t yn over the rows of one
+// Each group owns rows and its threads own columns, so the sums over rows stay
+// in registers: the sum S of t yn over the rows of one
 // gate row gives both dgate = scale w_post S and that gate row's share
 // scale gate S of dw_post; the sum of dh rn is dw_pre.  kSequence adds the
 // shares of dw_post in shared memory, at the end of each gate row; kElement
@@ -321,7 +356,7 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
 template <int V, int kMode>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const NormParams p) {
   extern __shared__ uint4 ring[];
-  __shared__ float part[kMaxWarps][2][3 * kMaxWarps];
+  __shared__ float part[2][4][kMaxWarps];
   constexpr int kArrays = kMode == kSingle ? 4 : 5;
   const int group = (int)(threadIdx.x >> 5) / p.warps, T = 32 * p.warps;
   const int t = threadIdx.x - group * T;
@@ -330,8 +365,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   // kSequence: this thread's columns of dw_post, after the ring
   float* post = reinterpret_cast<float*>(ring + (size_t)p.stages * kArrays * p.groups * p.nv) + 8 * (group * p.nv + t);
   const uint32_t c = blockIdx.x * p.groups + group;
-  const uint32_t m0 = c * p.chunk_rows < p.M ? c * p.chunk_rows : p.M;
-  const uint32_t m1 = m0 + p.chunk_rows < p.M ? m0 + p.chunk_rows : p.M;
+  const uint32_t step = kMode == kSequence ? 1 : p.step;
+  const uint32_t m0 = step == 1 ? (c * p.chunk_rows < p.M ? c * p.chunk_rows : p.M) : c;
+  const uint32_t m1 = step == 1 && m0 + p.chunk_rows < p.M ? m0 + p.chunk_rows : p.M;
   griddep_wait();
 
   auto fetch = [&](uint32_t row, int stage) {
@@ -352,7 +388,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
     }
     cp_async_commit();
   };
-  for (int s = 0; s < p.stages; ++s) fetch(m0 + s, s);
+  for (int s = 0; s < p.stages; ++s) fetch(m0 + s * step, s);
 
   F2 gw[V][4];  // scale w_post, times the gate when there is one row of it
   uint4 wq[V];
@@ -380,12 +416,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   int stage = 0;
   // the rows' statistics, one row ahead
   float pn_next = m0 < m1 ? __ldg(p.stats + m0) : 0.f, qn_next = m0 < m1 ? __ldg(p.stats + p.M + m0) : 0.f;
+  uint32_t it = 0;
 #pragma unroll 1
-  for (uint32_t m = m0; m < m1; ++m) {
+  for (uint32_t m = m0; m < m1; m += step, ++it) {
     const float pn = pn_next, qn = qn_next;
-    if (m + 1 < m1) {
-      pn_next = __ldg(p.stats + m + 1);
-      qn_next = __ldg(p.stats + p.M + m + 1);
+    if (m + step < m1) {
+      pn_next = __ldg(p.stats + m + step);
+      qn_next = __ldg(p.stats + p.M + m + step);
     }
     cp_async_wait(p.stages);
     const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
@@ -414,8 +451,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
         }
       }
     }
-    float s[3] = {sum(s0), sum(s1), sum(s2)};
-    group_sum<3>(s, part[group][m & 1], p.warps, group);
+    float s[4] = {sum(s0), sum(s1), sum(s2), 0.f};
+    group_sum4(s, part[it & 1], p.warps, group);
     const float k1 = qn * (s[0] * p.inv_d);                 // q m1
     const float k2 = fmaf(-k1, s[2], s[1]) * p.inv_d * pn;  // p m2
     const F2 nk1 = both(-k1), nk2 = both(-k2);
@@ -478,7 +515,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
         }
       }
     }
-    fetch(m + p.stages, stage);  // every read of the slot is done
+    fetch(m + p.stages * step, stage);  // every read of the slot is done
     if (++stage == p.stages) stage = 0;
   }
   griddep_launch_dependents();
@@ -569,7 +606,7 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const NormParams p, int 
 int check(const gemm_rs_norm_desc* d) {
   if (!d || d->gate_rows < 0 || !(d->eps >= 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->scale))
     return GEMM_RS_ERR_INVALID_ARG;
-  if (d->M < 0 || d->D <= 0 || d->D % 8 || d->D > GEMM_RS_NORM_MAX_D || d->M >= (1ll << 35) / d->D)
+  if (d->M < 0 || d->D <= 0 || d->D % 8 || d->D > GEMM_RS_NORM_MAX_D || d->M > (1ll << 34) / d->D)
     return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
   if (d->gate_rows > 0 && (d->M % d->gate_rows || (d->M > 0 && d->gate_rows > d->M)))
     return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
@@ -589,7 +626,7 @@ struct Split {
 Split split_of(const gemm_rs_norm_desc* d) {
   Split s;
   const GateMode mode = mode_of(d);
-  s.shape = shape_of((int)(d->D / 8), mode == kSingle ? 4 : 5, d->M, kBlocks, kMaxSmem, mode == kSequence ? 32 : 0);
+  s.shape = shape_of((int)(d->D / 8), mode == kSingle ? 4 : 5, d->M, kBlocks, kBackwardSmem, mode == kSequence ? 32 : 0);
   const long long lanes = (long long)kBlocks * s.shape.groups;
   s.chunk_rows = (d->M + lanes - 1) / lanes;
   if (s.chunk_rows < 1) s.chunk_rows = 1;
@@ -635,9 +672,9 @@ int launch(int grid, int threads, int smem, cudaStream_t st, Args... args) {
 }
 
 template <int V>
-int launch_forward(const NormParams& p, bool many_gates, int grid, int smem, cudaStream_t st) {
+int launch_forward(const NormParams& p, bool gate_ring, int grid, int smem, cudaStream_t st) {
   const int threads = 32 * p.warps * p.groups;
-  return many_gates ? launch<norm_forward_kernel<V, true>>(grid, threads, smem, st, p)
+  return gate_ring ? launch<norm_forward_kernel<V, true>>(grid, threads, smem, st, p)
                     : launch<norm_forward_kernel<V, false>>(grid, threads, smem, st, p);
 }
 template <int V>
@@ -669,20 +706,24 @@ extern "C" int gemm_rs_norm_forward(const gemm_rs_norm_desc* d, const void* x, c
   NormParams p = params_of(d);
   p.x = in(x); p.y = in(y); p.gate = in(gate); p.w_post = in(w_post); p.w_pre = in(w_pre);
   p.r = outp(r); p.h = outp(h); p.stats = static_cast<float*>(stats);
-  const bool many_gates = d->gate_rows > 1;
-  const int arrays = many_gates ? 3 : 2;
-  Shape s = shape_of(p.nv, arrays, d->M, 2 * sms, kMaxSmem / 2, 0);
+  // a gate row in registers pays from 8 rows on: loading it stalls its group
+  const bool gate_ring = d->gate_rows > 1 && p.rows_per_gate < 8;
+  const int arrays = gate_ring ? 3 : 2;
+  Shape s = shape_of(p.nv, arrays, d->M, 2 * sms, kMaxSmem / 2, 16);
   const int per_sm = forward_blocks(s.v);
-  if (per_sm == 1) s = shape_of(p.nv, arrays, d->M, sms, kMaxSmem, 0);
+  if (per_sm == 1) s = shape_of(p.nv, arrays, d->M, sms, kMaxSmem, 16);
   set_shape(&p, s);
-  const long long blocks = (d->M + s.groups - 1) / s.groups;
-  const int grid = (int)(blocks < (long long)per_sm * sms ? blocks : (long long)per_sm * sms);
+  const long long lanes = (long long)per_sm * sms * s.groups;
+  p.chunk_rows = (uint32_t)((d->M + lanes - 1) / lanes);
+  const long long chunks = (d->M + p.chunk_rows - 1) / p.chunk_rows;
+  const int grid = (int)((chunks + s.groups - 1) / s.groups);
+  p.step = d->gate_rows > 1 && !gate_ring ? 1 : (uint32_t)(grid * s.groups);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (s.v) {
-    case 1: return launch_forward<1>(p, many_gates, grid, s.smem, st);
-    case 2: return launch_forward<2>(p, many_gates, grid, s.smem, st);
-    case 3: return launch_forward<3>(p, many_gates, grid, s.smem, st);
-    default: return launch_forward<4>(p, many_gates, grid, s.smem, st);
+    case 1: return launch_forward<1>(p, gate_ring, grid, s.smem, st);
+    case 2: return launch_forward<2>(p, gate_ring, grid, s.smem, st);
+    case 3: return launch_forward<3>(p, gate_ring, grid, s.smem, st);
+    default: return launch_forward<4>(p, gate_ring, grid, s.smem, st);
   }
 }
 
@@ -735,6 +776,7 @@ extern "C" int gemm_rs_norm_backward(const gemm_rs_norm_desc* d, const void* dr,
   p.chunk_rows = (uint32_t)sp.chunk_rows;
   p.chunks = sp.chunks;
   p.blocks = sp.blocks;
+  p.step = mode_of(d) == kSequence ? 1 : (uint32_t)(sp.blocks * sp.shape.groups);
   set_shape(&p, sp.shape);
   const GateMode mode = mode_of(d);
   const long long plane = (long long)sp.blocks * d->D;

@@ -75,6 +75,10 @@ def inputs(M, D, gate_rows, seed=0):
     return t
 
 
+def bf16_ones(*shape):
+    return torch.ones(*shape, dtype=torch.bfloat16)
+
+
 def f64(t):
     return None if t is None else t.double().cpu().numpy()
 
@@ -90,11 +94,11 @@ def assert_close(got, ref, mag, steps, name):
                            f"{np.nanmax(np.abs(got - ref) / bound):.2f} x the bound")
 
 
-# rows and columns at the edges: one row, one vector, a ragged last warp, two to four vectors a thread,
+# rows and columns at the edges (gate rows of 7 and 8 rows too, where the gate's way in changes): one row, one vector, a ragged last warp, two to four vectors a thread,
 # fewer and more rows than chunks, gate rows that divide, straddle and equal the chunks
 SHAPES = [(1, 8, 0), (1, 8, 1), (3, 64, 3), (2, 264, 2), (5, 1000, 1), (1, 8192, 1), (152, 512, 8), (153, 520, 3),
           (304, 768, 4), (610, 256, 5), (700, 128, 350), (1003, 136, 1003), (960, 72, 6), (17, 4104, 0),
-          (9, 8200, 3), (6, 12288, 2), (4, 12296, 1), (5, 16384, 5), (1520, 1032, 10)]
+          (9, 8200, 3), (6, 12288, 2), (4, 12296, 1), (5, 16384, 5), (1520, 1032, 10), (2048, 520, 256), (1050, 264, 150)]
 
 
 @pytest.mark.gpu
@@ -168,6 +172,30 @@ def test_backward_matches_differences(M, D, gate_rows):
         # half a bf16 step and the fp32 error of every element; differences: 1e-7 of the terms' size
         bound = (np.abs(direction) * (2.0 ** -8 * np.abs(v) + (416 + M) * U * mag)).sum() + 1e-7 * np.abs(direction * mag).sum()
         assert abs(diff - (direction * f64(got[k])).sum()) <= bound, k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("left", [1.0, 0.1, 1e-3])
+def test_a_branch_that_cancels_the_residual(left):
+    """r is `left` of x: the sum of r^2 keeps its digits, whatever x and the branch are."""
+    M, D = 5, 1032
+    rng = np.random.default_rng(3)
+    t = inputs(M, D, 1, seed=3)
+    y = f64(t["y"])
+    p = 1 / np.sqrt((y * y).mean(1, keepdims=True) + 1e-6)
+    # w_post = gate = 1: the branch is y p; x is its negative, and a little more, in bf16 steps
+    t["w_post"], t["gate"] = bf16_ones(D), bf16_ones(1, D)
+    x = torch.from_numpy(-y * p * (1 - left) + 1e-4 * rng.standard_normal((M, D))).to(torch.bfloat16)
+    d = dev({**t, "x": x})
+    r, h, stats = block_norm.forward(d["x"], d["y"], d["w_post"], d["w_pre"], gate=d["gate"])
+    f = reference(f64(x), y, f64(t["w_post"]), f64(t["w_pre"]), f64(t["gate"]), 1.0, 1e-6)
+    mag = np.abs(f64(x)) + np.abs(f["c"])
+    # an error of 256 * 2**-24 of the terms in each r, and so (by the mean) in q
+    drift = 256 * U * np.sqrt((mag * mag).mean(1)) * f["q"][:, 0]
+    assert (np.abs(f64(stats[1]) / f["q"][:, 0] - 1) <= 2 * drift).all()
+    assert_close(r, f["r"], mag, 256, "r")
+    assert_close(h, f["h"], (mag * f["q"] + np.abs(f["r"] * f["q"]) * drift[:, None] / (256 * U)) * np.abs(f64(t["w_pre"])) * 2,
+                 256, "h")
 
 
 @pytest.mark.gpu
