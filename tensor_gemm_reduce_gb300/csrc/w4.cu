@@ -10,9 +10,13 @@
 // into its fragments (tcgen05 would need them written to shared memory as bf16,
 // four times the bytes read from HBM), and its rate is not the limit.
 //
-// Unpacking: code c in the low bits of 0x4300 is the bf16 128 + c; subtracting
-// 128 + zero is exact, so the tensor core multiplies exact integers with the
-// bf16 inputs.  Each group's sum is scaled in fp32 and added to the total.
+// Unpacking: a bf16 pattern below 256 stands for 2^-133 times its value (bf16's
+// subnormals and its first binade lie on one line), so a code masked out of a
+// word is a number already, wherever it lies in the low byte of a half word.
+// One bf16x2 FMA, exact, scales it and subtracts the zero point: the tensor core
+// multiplies the exact values (code - zero) 2^-6 with the bf16 inputs.  Each
+// group's sum is scaled in fp32 (by 2^6 too) and added to the total.  The masks
+// and shifts keep the integer pipe the busiest: 5 instructions for 8 weights.
 //
 // Split: a cluster of 8 CTAs computes 128 columns, CTA r rank r's share of the
 // sum; the eight fp32 partial sums are exchanged through distributed shared
@@ -25,40 +29,54 @@ using namespace grs;
 namespace {
 
 constexpr int kRanks = 8;
-constexpr int kWarps = 8;           // each 16 columns
-constexpr int kTileN = 16 * kWarps;
+constexpr int kWarps = 4;
+constexpr int kHalves = 2;          // 16-column halves of the 32 columns that a warp multiplies
+constexpr int kBlockN = 16 * kHalves;
+constexpr int kTileN = kWarps * kBlockN;
 constexpr int kCell = 64;           // inner elements of a lane's 16-byte load
+constexpr int kUnit = 128;          // inner elements of a step: two cells of each half
 constexpr int kMaxTokens = 32;
-constexpr int kDepth = 3;           // units (2 cells) of weights in flight per warp
 constexpr int kMaxParts = 8;
 
-// Packed buffer: weights [N/16][8][cells][32 lanes] of 16 bytes, then scales
-// [N/16][8][groups][8] of two bf16 (columns g and g + 8), then zero points
-// [N/16][8][groups][8] of two bytes; N/16 rounded up, cells = K/8/64 rounded up.
-// A cell's 64 inner elements: step j of half h holds, in lane 4 g + q, inner
+// Inner elements of a chunk of the inputs in shared memory, for `tiles` tiles
+// of 8 tokens, and its row pitch in bytes (64 beyond a multiple of 128, so that
+// the two rows that 8 lanes read lie in different banks).
+__host__ __device__ constexpr int chunk_of(int tiles) { return 1024 / tiles; }
+__host__ __device__ constexpr int pitch_of(int tiles) { return 2 * chunk_of(tiles) + 64; }
+// Units of weights in flight for each warp (2 KiB each), as the registers allow.
+__host__ __device__ constexpr int depth_of(int tiles) { return tiles == 1 ? 3 : 2; }
+// CTAs that share an SM; at 4 the 512 CTAs of 8192 columns all run at once.
+__host__ __device__ constexpr int blocks_of(int tiles) { return tiles <= 2 ? 4 : 3; }
+
+// Packed buffer: weights [N/32][8][units][2 halves][2 cells][32 lanes] of 16
+// bytes, then scales [N/32][8][groups][2 halves][8] of two bf16 (columns g and
+// g + 8), then zero points of the same shape, two bytes each; N/32 and units =
+// K/8/128 rounded up, groups those of whole units.  What lies beyond the layer's
+// sizes is zero.
+// A cell's 64 inner elements: step j of part h holds, in lane 4 g + q, inner
 // elements 32 h + 8 q + 4 j + {0, 1, 2, 3} of columns g and g + 8, four bits
 // each, at bits 0, 16 (column g, elements 0, 1), 4, 20 (g + 8), 8, 24 (column
 // g, elements 2, 3) and 12, 28 of word 2 h + j.
 struct Layout {
-  long long blocks, cells, groups;
+  long long blocks, units, groups;
   long long scale_off, zero_off, bytes;
 };
 Layout layout_of(int64_t N, int64_t K, int group, bool zeros) {
   Layout l;
   const int64_t Kr = K / kRanks;
-  l.blocks = (N + 15) / 16;
-  l.cells = (Kr + kCell - 1) / kCell;
-  l.groups = (Kr + group - 1) / group;
-  l.scale_off = l.blocks * kRanks * l.cells * 512;
-  l.zero_off = l.scale_off + l.blocks * kRanks * l.groups * 32;
-  l.bytes = l.zero_off + (zeros ? l.blocks * kRanks * l.groups * 16 : 0);
+  l.blocks = (N + kBlockN - 1) / kBlockN;
+  l.units = (Kr + kUnit - 1) / kUnit;
+  l.groups = l.units * (kUnit / group);
+  l.scale_off = l.blocks * kRanks * l.units * 2048;
+  l.zero_off = l.scale_off + l.blocks * kRanks * l.groups * 64;
+  l.bytes = l.zero_off + (zeros ? l.blocks * kRanks * l.groups * 32 : 0);
   return l;
 }
 
 struct W4Params {
   int M, N, Kr, group;
-  int blocks, cells, groups;
-  int parts, part_cells;       // the cells of a rank are cut into parts of part_cells
+  int blocks, units, groups;   // units and groups of a rank
+  int parts, part_units;       // the units of a rank are cut into parts of part_units
   const uint16_t* x;           // [8][M][Kr]
   const uint4* weights;
   const uint32_t* scales;
@@ -74,10 +92,18 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
@@ -87,102 +113,166 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 
 // kTiles tiles of 8 tokens, groups of kGroup inner elements.
 template <int kTiles, int kGroup, bool kZeros>
-__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps)
+__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, blocks_of(kTiles))
     w4_kernel(const W4Params p) {
-  __shared__ float sums[kTiles * 8 * kTileN];  // this rank's share: [token][column]
+  // two chunks of the inputs [token][chunk]; then this rank's share [token][column]
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kChunk = chunk_of(kTiles), kPitch = pitch_of(kTiles), kDepth = depth_of(kTiles);
+  constexpr int kPerUnit = kUnit / kGroup;  // groups in a unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x, tile = blockIdx.y, part = blockIdx.z;
   const int g = lane >> 2, q = lane & 3;
-  const int block = tile * kWarps + warp;
-  const int c0 = part * p.part_cells;
-  const int c1 = c0 + p.part_cells < p.cells ? c0 + p.part_cells : p.cells;
+  const int u0 = part * p.part_units;
+  const int u1 = u0 + p.part_units < p.units ? u0 + p.part_units : p.units;
+  const uint32_t sbase = smem_u32(smem);
+  griddep_wait();
 
-  float acc[kTiles][4];
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+  // inputs of units [u, u + kChunk / kUnit) into buffer `buf`; zero beyond the row's end
+  auto stage_inputs = [&](int u, int buf) {
+    const int k0 = u * kUnit;
+    const int vectors = (u1 - u) * kUnit < kChunk ? (u1 - u) * (kUnit / 8) : kChunk / 8;
+    for (int i = threadIdx.x; i < p.M * vectors; i += blockDim.x) {
+      const int m = i / vectors, k = (i - m * vectors) * 8;
+      const uint32_t dst = sbase + (uint32_t)((buf * p.M + m) * kPitch + 2 * k);
+      const uint16_t* src = p.x + ((long long)rank * p.M + m) * p.Kr + k0 + k;
+      const bool in = k0 + k < p.Kr;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(in ? src : p.x),
+                   "r"(in ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 
-  if (block < p.blocks && c0 < c1) {
-    const long long at = (long long)block * kRanks + rank;
-    const uint4* w = p.weights + at * p.cells * 32 + lane;
-    const uint32_t* sc = p.scales + at * p.groups * 8 + g;
-    const uint16_t* zp = kZeros ? p.zeros + at * p.groups * 8 + g : nullptr;
-    const uint16_t* x = p.x + (long long)rank * p.M * p.Kr + 8 * q;
-    uint4 buf[kDepth][2];
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    auto fetch = [&](uint4 (&u)[2], int c) {
-      u[0] = c < c1 ? __ldcs(w + (long long)c * 32) : none;
-      u[1] = c + 1 < c1 ? __ldcs(w + (long long)(c + 1) * 32) : none;
-    };
+  float acc[kHalves][kTiles][4];
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) fetch(buf[d], c0 + 2 * d);
+  for (int b = 0; b < kHalves; ++b)
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[b][t][i] = 0.f;
+
+  // A unit's weights, scales and zero points.  Lane 4 g + q holds those of the
+  // unit's group q (columns g and g + 8); the others ask it by a shuffle.
+  struct Unit {
+    uint4 w[kHalves][2];
+    uint32_t s[kHalves], z[kHalves];
+  };
+  // columns beyond the last block read the last one's weights and are not stored
+  const int block = tile * kWarps + warp < p.blocks ? tile * kWarps + warp : p.blocks - 1;
+  const long long at = (long long)block * kRanks + rank;
+  const long long group0 = at * p.groups + (long long)u0 * kPerUnit + q % kPerUnit;
+  const uint4* wp = p.weights + (at * p.units + u0) * 128 + lane;
+  const uint32_t* sp = p.scales + group0 * 16 + g;
+  const uint16_t* zp = kZeros ? p.zeros + group0 * 16 + g : nullptr;
+  // unit `d` beyond the pointers
+  auto fetch = [&](Unit& v, int d, bool in) {
+    if (!in) return;
+#pragma unroll
+    for (int b = 0; b < kHalves; ++b) {
+      v.w[b][0] = __ldcs(wp + d * 128 + b * 64);
+      v.w[b][1] = __ldcs(wp + d * 128 + b * 64 + 32);
+      v.s[b] = __ldcs(sp + d * kPerUnit * 16 + 8 * b);
+      if (kZeros) v.z[b] = __ldcs(zp + d * kPerUnit * 16 + 8 * b);
+    }
+  };
+  Unit ring[kDepth];
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) fetch(ring[d], d, u0 + d < u1);
+  stage_inputs(u0, 0);
+
+  // tokens beyond the last read its row; their columns are not stored
+  uint32_t row[kTiles];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) row[t] = (uint32_t)((8 * t + g < p.M ? 8 * t + g : p.M - 1) * kPitch + 16 * q);
+
+  int buf = 0;
+  uint32_t xu = 0;  // the unit's inputs
+  constexpr int kChunkUnits = kChunk / kUnit;
 #pragma unroll 1
-    for (int base = c0; base < c1; base += 2 * kDepth) {
+  for (int base = u0; base < u1; base += kDepth) {
+    wp += kDepth * 128;
+    sp += kDepth * kPerUnit * 16;
+    if (kZeros) zp += kDepth * kPerUnit * 16;
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        const int c = base + 2 * d;
-        if (c >= c1) break;
-        const uint4 cur[2] = {buf[d][0], buf[d][1]};
-        fetch(buf[d], c + 2 * kDepth);
-        float sum[kTiles][4];
+    for (int d = 0; d < kDepth; ++d) {
+      const int u = base + d;
+      if (u >= u1) break;
+      if ((u - u0) % kChunkUnits == 0) {  // the chunk has arrived; the next one takes the other buffer
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        xu = sbase + (uint32_t)(buf * p.M * kPitch);
+        buf ^= 1;
+        if (u + kChunkUnits < u1) stage_inputs(u + kChunkUnits, buf);
+      } else {
+        xu += 2 * kUnit;
+      }
+      const Unit cur = ring[d];
+      fetch(ring[d], d, u + kDepth < u1);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {  // 32 inner elements
-          const int k = c * kCell + 32 * h;
-          const int grp = k / kGroup;
-          if (h % (kGroup / 32) == 0) {
+      for (int grp = 0; grp < kPerUnit; ++grp) {
+        float sum[kHalves][kTiles][4];
+        uint32_t nz[kHalves][2];  // -(zero point) 2^-6 of columns g and g + 8, in both halves
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t)
+        for (int b = 0; b < kHalves; ++b) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) sum[t][i] = 0.f;
+          for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[b][t][i] = 0.f;
+          nz[b][0] = nz[b][1] = 0xBE00BE00u;  // -8 2^-6
+          if (kZeros) {
+            const uint32_t z = __shfl_sync(0xffffffffu, cur.z[b], (lane & 28) + grp);
+            // z as a number (its pattern is 2^-133 z) times -2^127
+            nz[b][0] = fma_bf16x2((z & 0xFFu) * 0x10001u, 0xFF00FF00u, 0u);
+            nz[b][1] = fma_bf16x2((z >> 8) * 0x10001u, 0xFF00FF00u, 0u);
           }
-          // 128 + zero point of columns g and g + 8, in both halves
-          uint32_t z0 = 0x43084308u, z1 = 0x43084308u;
-          if (kZeros && grp < p.groups) {
-            const uint32_t z = __ldg(zp + grp * 8);
-            z0 = 0x43004300u | (z & 0xFFu) * 0x10001u;
-            z1 = 0x43004300u | (z >> 8) * 0x10001u;
-          }
+        }
+#pragma unroll
+        for (int hh = 0; hh < kGroup / 32; ++hh) {  // 32 inner elements
+          const int h = grp * (kGroup / 32) + hh;
           uint4 xv[kTiles];
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            const int m = 8 * t + g;
-            xv[t] = m < p.M && k + 8 * q < p.Kr
-                        ? __ldg(reinterpret_cast<const uint4*>(x + (long long)m * p.Kr + k))
-                        : none;
-          }
+          for (int t = 0; t < kTiles; ++t) xv[t] = ld_shared_v4(xu + row[t] + 64u * h);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint4& v = cur[h >> 1];
-            const uint32_t word = (h & 1) ? (j ? v.w : v.z) : (j ? v.y : v.x);
-            uint32_t a[4];
+          for (int b = 0; b < kHalves; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              a[i] = sub_bf16x2(((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u, (i & 1) ? z1 : z0);
+            for (int j = 0; j < 2; ++j) {
+              const uint4& v = cur.w[b][h >> 1];
+              const uint32_t word = (h & 1) ? (j ? v.w : v.z) : (j ? v.y : v.x), high = word >> 8;
+              const uint32_t a[4] = {fma_bf16x2(word & 0x000F000Fu, 0x7F007F00u, nz[b][0]),   // 2^127
+                                     fma_bf16x2(word & 0x00F000F0u, 0x7D007D00u, nz[b][1]),   // 2^123
+                                     fma_bf16x2(high & 0x000F000Fu, 0x7F007F00u, nz[b][0]),
+                                     fma_bf16x2(high & 0x00F000F0u, 0x7D007D00u, nz[b][1])};
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-              mma_16816(sum[t], a, j ? xv[t].z : xv[t].x, j ? xv[t].w : xv[t].y);
-          }
-          if ((h + 1) % (kGroup / 32) == 0) {
-            const uint32_t s = grp < p.groups ? __ldg(sc + grp * 8) : 0u;
-            const float s0 = bf16lo_to_f32(s), s1 = bf16hi_to_f32(s);
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-              acc[t][0] = fmaf(s0, sum[t][0], acc[t][0]);
-              acc[t][1] = fmaf(s0, sum[t][1], acc[t][1]);
-              acc[t][2] = fmaf(s1, sum[t][2], acc[t][2]);
-              acc[t][3] = fmaf(s1, sum[t][3], acc[t][3]);
+              for (int t = 0; t < kTiles; ++t)
+                mma_16816(sum[b][t], a, j ? xv[t].z : xv[t].x, j ? xv[t].w : xv[t].y);
             }
+        }
+#pragma unroll
+        for (int b = 0; b < kHalves; ++b) {
+          const uint32_t s = __shfl_sync(0xffffffffu, cur.s[b], (lane & 28) + grp);
+          const float s0 = 64.f * bf16lo_to_f32(s), s1 = 64.f * bf16hi_to_f32(s);
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            acc[b][t][0] = fmaf(s0, sum[b][t][0], acc[b][t][0]);
+            acc[b][t][1] = fmaf(s0, sum[b][t][1], acc[b][t][1]);
+            acc[b][t][2] = fmaf(s1, sum[b][t][2], acc[b][t][2]);
+            acc[b][t][3] = fmaf(s1, sum[b][t][3], acc[b][t][3]);
           }
         }
       }
     }
   }
+  __syncthreads();  // every read of the inputs is done
+  float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t)
+  for (int b = 0; b < kHalves; ++b)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      sums[(8 * t + 2 * q + (i & 1)) * kTileN + warp * 16 + g + 8 * (i >> 1)] = acc[t][i];
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = 8 * t + 2 * q + (i & 1);
+        if (m < p.M) sums[m * kTileN + (warp * kHalves + b) * 16 + g + 8 * (i >> 1)] = acc[b][t][i];
+      }
   cluster_sync();  // every rank's share is in its shared memory
 
   // CTA r adds columns [16 r, 16 r + 16) in rank order
@@ -222,7 +312,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps)
 }
 
 struct PackParams {
-  int N, Kr, group, blocks, cells, groups;
+  int N, Kr, group, blocks, units, groups, in_groups;
   const uint8_t* codes;    // [8][Kr][N]
   const uint16_t* scales;  // [8][groups][N]
   const uint8_t* zeros;    // [8][groups][N] or null
@@ -235,37 +325,40 @@ struct PackParams {
 __global__ void __launch_bounds__(256) w4_pack_kernel(const PackParams p) {
   const long long stride = (long long)gridDim.x * blockDim.x;
   const long long first = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long words = (long long)p.blocks * kRanks * p.cells * 128;
+  const long long words = (long long)p.blocks * kRanks * p.units * 512;
   for (long long i = first; i < words; i += stride) {
     const int step = (int)(i & 3), lane = (int)(i >> 2) & 31;
     const long long cell = i >> 7;
-    const int c = (int)(cell % p.cells);
-    const int r = (int)(cell / p.cells % kRanks);
-    const int block = (int)(cell / p.cells / kRanks);
+    const int half = (int)(cell >> 1) & 1;
+    const long long unit = cell >> 2;
+    const int c = (int)(unit % p.units) * 2 + (int)(cell & 1);
+    const int r = (int)(unit / p.units % kRanks);
+    const int block = (int)(unit / p.units / kRanks);
     const int k0 = c * kCell + 32 * (step >> 1) + 8 * (lane & 3) + 4 * (step & 1);
     uint32_t w = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int i4 = e >> 1;  // MMA register: column g or g + 8, inner pair 0 or 1
-      const int n = block * 16 + (lane >> 2) + 8 * (i4 & 1);
+      const int n = block * kBlockN + half * 16 + (lane >> 2) + 8 * (i4 & 1);
       const int k = k0 + 2 * (i4 >> 1) + (e & 1);
       if (n < p.N && k < p.Kr)
         w |= (uint32_t)(p.codes[((long long)r * p.Kr + k) * p.N + n] & 15u) << (4 * i4 + 16 * (e & 1));
     }
     p.weights[i] = w;
   }
-  const long long metas = (long long)p.blocks * kRanks * p.groups * 8;
+  const long long metas = (long long)p.blocks * kRanks * p.groups * 16;
   for (long long i = first; i < metas; i += stride) {
-    const int g = (int)(i & 7);
-    const long long t = i >> 3;
+    const int g = (int)(i & 7), half = (int)(i >> 3) & 1;
+    const long long t = i >> 4;
     const int grp = (int)(t % p.groups);
     const int r = (int)(t / p.groups % kRanks);
-    const int n = (int)(t / p.groups / kRanks) * 16 + g;
-    const long long row = ((long long)r * p.groups + grp) * p.N;
-    const uint32_t lo = n < p.N ? p.scales[row + n] : 0u, hi = n + 8 < p.N ? p.scales[row + n + 8] : 0u;
+    const int n = (int)(t / p.groups / kRanks) * kBlockN + half * 16 + g;
+    const long long row = ((long long)r * p.in_groups + grp) * p.N;
+    const bool lo_in = grp < p.in_groups && n < p.N, hi_in = grp < p.in_groups && n + 8 < p.N;
+    const uint32_t lo = lo_in ? p.scales[row + n] : 0u, hi = hi_in ? p.scales[row + n + 8] : 0u;
     p.out_scales[i] = lo | hi << 16;
     if (p.zeros) {
-      const uint32_t zl = n < p.N ? p.zeros[row + n] & 127u : 0u, zh = n + 8 < p.N ? p.zeros[row + n + 8] & 127u : 0u;
+      const uint32_t zl = lo_in ? p.zeros[row + n] & 127u : 0u, zh = hi_in ? p.zeros[row + n + 8] & 127u : 0u;
       p.out_zeros[i] = (uint16_t)(zl | zh << 8);
     }
   }
@@ -307,27 +400,28 @@ int check(int64_t M, int64_t N, int64_t K, int group) {
   return GEMM_RS_OK;
 }
 
-// Few columns leave SMs idle: the inner dimension is then cut into parts (of
-// an even number of cells, so that a group stays whole).
-void split_of(const Layout& l, int64_t N, int* parts, int* part_cells) {
+// Few columns leave SMs idle: the inner dimension is then cut into parts.
+void split_of(const Layout& l, int64_t N, int* parts, int* part_units) {
   const long long ctas = (N + kTileN - 1) / kTileN * kRanks;
   long long want = ctas > 0 ? 304 / ctas : 1;
-  const long long units = (l.cells + 1) / 2;
+  const long long units = l.units;
   if (want > kMaxParts) want = kMaxParts;
-  if (want > units / 4) want = units / 4;  // at least 8 cells (4 KiB a warp) in a part
+  if (want > units / 4) want = units / 4;  // at least 4 units (8 KiB a warp) in a part
   if (want < 1) want = 1;
   const long long per = (units + want - 1) / want;
-  *part_cells = (int)(2 * per);
+  *part_units = (int)per;
   *parts = (int)(per > 0 ? (units + per - 1) / per : 1);
   if (*parts < 1) *parts = 1;
 }
 
 template <int kTiles, int kGroup>
 void launch(const W4Params& p, dim3 grid, cudaStream_t st) {
+  const int inputs = 2 * p.M * pitch_of(kTiles), sums = p.M * kTileN * 4;
+  const int smem = inputs > sums ? inputs : sums;  // under 48 KB for every token count
   if (p.zeros)
-    w4_kernel<kTiles, kGroup, true><<<grid, 32 * kWarps, 0, st>>>(p);
+    w4_kernel<kTiles, kGroup, true><<<grid, 32 * kWarps, smem, st>>>(p);
   else
-    w4_kernel<kTiles, kGroup, false><<<grid, 32 * kWarps, 0, st>>>(p);
+    w4_kernel<kTiles, kGroup, false><<<grid, 32 * kWarps, smem, st>>>(p);
 }
 template <int kTiles>
 void launch(const W4Params& p, dim3 grid, cudaStream_t st) {
@@ -348,8 +442,8 @@ extern "C" int gemm_rs_w4_bytes(int64_t N, int64_t K, int group, int has_zeros, 
   const Layout l = layout_of(N, K, group, has_zeros != 0);
   if (weight_bytes) *weight_bytes = (size_t)l.bytes;
   if (workspace_bytes) {
-    int parts = 1, cells = 0;
-    split_of(l, N, &parts, &cells);
+    int parts = 1, part_units = 0;
+    split_of(l, N, &parts, &part_units);
     const size_t tiles = (size_t)(N + kTileN - 1) / kTileN;
     *workspace_bytes = tiles * kRanks * 4 + (parts > 1 ? (size_t)parts * kMaxTokens * tiles * kTileN * 4 : 0);
   }
@@ -366,10 +460,10 @@ extern "C" int gemm_rs_w4_quantize(int64_t N, int64_t K, int group, const void* 
   int sms = 0;
   rc = current_device_sms(&sms);
   if (rc) return rc;
-  const Layout l = layout_of(N, K, group, false);
+  const int groups = (int)((K / kRanks + group - 1) / group);
   w4_quantize_kernel<<<8 * sms, 256, 0, static_cast<cudaStream_t>(stream)>>>(
       static_cast<const uint16_t*>(W), static_cast<uint8_t*>(codes), static_cast<uint16_t*>(scales), (int)N,
-      (int)(K / kRanks), group, (int)l.groups);
+      (int)(K / kRanks), group, groups);
   return launch_status();
 }
 
@@ -386,7 +480,8 @@ extern "C" int gemm_rs_w4_pack(int64_t N, int64_t K, int group, const void* code
   if (rc) return rc;
   const Layout l = layout_of(N, K, group, zeros != nullptr);
   uint8_t* base = static_cast<uint8_t*>(weight);
-  PackParams p = {(int)N, (int)(K / kRanks), group, (int)l.blocks, (int)l.cells, (int)l.groups,
+  PackParams p = {(int)N, (int)(K / kRanks), group, (int)l.blocks, (int)l.units, (int)l.groups,
+                  (int)((K / kRanks + group - 1) / group),
                   static_cast<const uint8_t*>(codes), static_cast<const uint16_t*>(scales),
                   static_cast<const uint8_t*>(zeros), reinterpret_cast<uint32_t*>(base),
                   reinterpret_cast<uint32_t*>(base + l.scale_off), reinterpret_cast<uint16_t*>(base + l.zero_off)};
@@ -421,9 +516,9 @@ extern "C" int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int ha
   p.Kr = (int)(K / kRanks);
   p.group = group;
   p.blocks = (int)l.blocks;
-  p.cells = (int)l.cells;
   p.groups = (int)l.groups;
-  split_of(l, N, &p.parts, &p.part_cells);
+  p.units = (int)l.units;
+  split_of(l, N, &p.parts, &p.part_units);
   p.x = static_cast<const uint16_t*>(x);
   p.weights = reinterpret_cast<const uint4*>(base);
   p.scales = reinterpret_cast<const uint32_t*>(base + l.scale_off);
