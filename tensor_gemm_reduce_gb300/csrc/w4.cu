@@ -15,13 +15,12 @@
 // word is a number already, wherever it lies in the low byte of a half word.
 // One bf16x2 FMA, exact, scales it and subtracts the zero point: the tensor core
 // multiplies the exact values (code - zero) 2^-6 with the bf16 inputs.  Each
-// group's sum is scaled in fp32 (by 2^6 too) and added to the total.  The masks
+// group's sum is scaled in fp32 and added to the total, which takes 2^6 at the end.  The masks
 // and shifts keep the integer pipe the busiest: 5 instructions for 8 weights.
 //
 // Split: a cluster of 8 CTAs computes 128 columns, CTA r rank r's share of the
 // sum; the eight fp32 partial sums are exchanged through distributed shared
-// memory and CTA r writes columns [16 r, 16 r + 16) of the 128, added in rank
-// order: the layer's reduce-scatter, inside one cluster.
+// memory and CTA r writes an eighth of the columns, added in rank order: the layer's reduce-scatter, inside one cluster.
 #include "ops_common.cuh"
 
 using namespace grs;
@@ -33,6 +32,7 @@ constexpr int kWarps = 4;
 constexpr int kHalves = 2;          // 16-column halves of the 32 columns that a warp multiplies
 constexpr int kBlockN = 16 * kHalves;
 constexpr int kTileN = kWarps * kBlockN;
+constexpr int kShare = kTileN / kRanks;  // columns that a CTA of the cluster writes
 constexpr int kCell = 64;           // inner elements of a lane's 16-byte load
 constexpr int kUnit = 128;          // inner elements of a step: two cells of each half
 constexpr int kMaxTokens = 32;
@@ -44,7 +44,7 @@ constexpr int kMaxParts = 8;
 __host__ __device__ constexpr int chunk_of(int tiles) { return 1024 / tiles; }
 __host__ __device__ constexpr int pitch_of(int tiles) { return 2 * chunk_of(tiles) + 64; }
 // Units of weights in flight for each warp (2 KiB each), as the registers allow.
-__host__ __device__ constexpr int depth_of(int tiles) { return tiles == 1 ? 3 : 2; }
+__host__ __device__ constexpr int depth_of(int tiles) { return tiles <= 2 ? 3 : 2; }
 // CTAs that share an SM; at 4 the 512 CTAs of 8192 columns all run at once.
 __host__ __device__ constexpr int blocks_of(int tiles) { return tiles <= 2 ? 4 : 3; }
 
@@ -87,10 +87,17 @@ struct W4Params {
 };
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d = a b: the same without an addend.
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
@@ -206,21 +213,16 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, bl
       } else {
         xu += 2 * kUnit;
       }
-      const Unit cur = ring[d];
-      fetch(ring[d], d, u + kDepth < u1);
+      const Unit& cur = ring[d];
 #pragma unroll
       for (int grp = 0; grp < kPerUnit; ++grp) {
         float sum[kHalves][kTiles][4];
         uint32_t nz[kHalves][2];  // -(zero point) 2^-6 of columns g and g + 8, in both halves
 #pragma unroll
         for (int b = 0; b < kHalves; ++b) {
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[b][t][i] = 0.f;
           nz[b][0] = nz[b][1] = 0xBE00BE00u;  // -8 2^-6
           if (kZeros) {
-            const uint32_t z = __shfl_sync(0xffffffffu, cur.z[b], (lane & 28) + grp);
+            const uint32_t z = kPerUnit == 1 ? cur.z[b] : __shfl_sync(0xffffffffu, cur.z[b], (lane & 28) + grp);
             // z as a number (its pattern is 2^-133 z) times -2^127
             nz[b][0] = fma_bf16x2((z & 0xFFu) * 0x10001u, 0xFF00FF00u, 0u);
             nz[b][1] = fma_bf16x2((z >> 8) * 0x10001u, 0xFF00FF00u, 0u);
@@ -243,14 +245,18 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, bl
                                      fma_bf16x2(high & 0x000F000Fu, 0x7F007F00u, nz[b][0]),
                                      fma_bf16x2(high & 0x00F000F0u, 0x7D007D00u, nz[b][1])};
 #pragma unroll
-              for (int t = 0; t < kTiles; ++t)
-                mma_16816(sum[b][t], a, j ? xv[t].z : xv[t].x, j ? xv[t].w : xv[t].y);
+              for (int t = 0; t < kTiles; ++t) {
+                if (hh == 0 && j == 0)
+                  mma_16816_first(sum[b][t], a, xv[t].x, xv[t].y);
+                else
+                  mma_16816(sum[b][t], a, j ? xv[t].z : xv[t].x, j ? xv[t].w : xv[t].y);
+              }
             }
         }
 #pragma unroll
         for (int b = 0; b < kHalves; ++b) {
-          const uint32_t s = __shfl_sync(0xffffffffu, cur.s[b], (lane & 28) + grp);
-          const float s0 = 64.f * bf16lo_to_f32(s), s1 = 64.f * bf16hi_to_f32(s);
+          const uint32_t s = kPerUnit == 1 ? cur.s[b] : __shfl_sync(0xffffffffu, cur.s[b], (lane & 28) + grp);
+          const float s0 = bf16lo_to_f32(s), s1 = bf16hi_to_f32(s);
 #pragma unroll
           for (int t = 0; t < kTiles; ++t) {
             acc[b][t][0] = fmaf(s0, sum[b][t][0], acc[b][t][0]);
@@ -260,6 +266,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, bl
           }
         }
       }
+      fetch(ring[d], d, u + kDepth < u1);  // into the registers just used
     }
   }
   __syncthreads();  // every read of the inputs is done
@@ -271,14 +278,14 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, bl
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int m = 8 * t + 2 * q + (i & 1);
-        if (m < p.M) sums[m * kTileN + (warp * kHalves + b) * 16 + g + 8 * (i >> 1)] = acc[b][t][i];
+        if (m < p.M) sums[m * kTileN + (warp * kHalves + b) * 16 + g + 8 * (i >> 1)] = 64.f * acc[b][t][i];
       }
   cluster_sync();  // every rank's share is in its shared memory
 
-  // CTA r adds columns [16 r, 16 r + 16) in rank order
+  // CTA r adds its kShare columns of the tile in rank order
   const uint32_t mine = smem_u32(sums);
-  for (int i = threadIdx.x; i < 16 * p.M; i += blockDim.x) {
-    const int m = i >> 4, col = rank * 16 + (i & 15);
+  for (int i = threadIdx.x; i < kShare * p.M; i += blockDim.x) {
+    const int m = i / kShare, col = rank * kShare + i % kShare;
     const int n = tile * kTileN + col;
     float s = 0.f;
 #pragma unroll
@@ -300,8 +307,8 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, bl
   __syncthreads();
   if (!last) return;
   __threadfence();
-  for (int i = threadIdx.x; i < 16 * p.M; i += blockDim.x) {
-    const int m = i >> 4, n = tile * kTileN + rank * 16 + (i & 15);
+  for (int i = threadIdx.x; i < kShare * p.M; i += blockDim.x) {
+    const int m = i / kShare, n = tile * kTileN + rank * kShare + i % kShare;
     if (n >= p.N) continue;
     float s = 0.f;
     for (int z = 0; z < p.parts; ++z)
