@@ -28,10 +28,8 @@ using namespace grs;
 namespace {
 
 constexpr int kRanks = 8;
-constexpr int kWarps = 4;
-constexpr int kHalves = 2;          // 16-column halves of the 32 columns that a warp multiplies
-constexpr int kBlockN = 16 * kHalves;
-constexpr int kTileN = kWarps * kBlockN;
+constexpr int kBlockN = 32;         // columns that lie together in the packed weights, in two halves
+constexpr int kTileN = 4 * kBlockN; // columns of a cluster
 constexpr int kShare = kTileN / kRanks;  // columns that a CTA of the cluster writes
 constexpr int kCell = 64;           // inner elements of a lane's 16-byte load
 constexpr int kUnit = 128;          // inner elements of a step: two cells of each half
@@ -41,12 +39,16 @@ constexpr int kMaxParts = 8;
 // Inner elements of a chunk of the inputs in shared memory, for `tiles` tiles
 // of 8 tokens, and its row pitch in bytes (64 beyond a multiple of 128, so that
 // the two rows that 8 lanes read lie in different banks).
-__host__ __device__ constexpr int chunk_of(int tiles) { return 1024 / tiles; }
+__host__ __device__ constexpr int chunk_of(int tiles) { return tiles > 2 ? 128 : 1024 / tiles; }
 __host__ __device__ constexpr int pitch_of(int tiles) { return 2 * chunk_of(tiles) + 64; }
-// Units of weights in flight for each warp (2 KiB each), as the registers allow.
-__host__ __device__ constexpr int depth_of(int tiles) { return tiles <= 2 ? 3 : 2; }
-// CTAs that share an SM; at 4 the 512 CTAs of 8192 columns all run at once.
-__host__ __device__ constexpr int blocks_of(int tiles) { return tiles <= 2 ? 4 : 3; }
+// Halves of a block that a warp multiplies (one set of input fragments serves
+// both, but 3 and 4 token tiles leave no registers for a second one), warps of a
+// CTA, units of weights in flight for each warp, and CTAs that share an SM: at 4
+// (2 of twice the warps) the 512 CTAs of 8192 columns all run at once.
+__host__ __device__ constexpr int halves_of(int tiles) { return tiles <= 2 ? 2 : 1; }
+__host__ __device__ constexpr int warps_of(int tiles) { return kTileN / 16 / halves_of(tiles); }
+__host__ __device__ constexpr int depth_of(int tiles) { return tiles <= 2 ? 3 : 4; }
+__host__ __device__ constexpr int ctas_of(int tiles) { return 16 / warps_of(tiles); }
 
 // Packed buffer: weights [N/32][8][units][2 halves][2 cells][32 lanes] of 16
 // bytes, then scales [N/32][8][groups][2 halves][8] of two bf16 (columns g and
@@ -104,26 +106,18 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // kTiles tiles of 8 tokens, groups of kGroup inner elements.
 template <int kTiles, int kGroup, bool kZeros>
-__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, blocks_of(kTiles))
+__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * warps_of(kTiles), ctas_of(kTiles))
     w4_kernel(const W4Params p) {
-  // two chunks of the inputs [token][chunk]; then this rank's share [token][column]
+  // two chunks of the inputs [token][chunk], then the ranks' shares of this CTA's
+  // columns [rank][token][kShare], which their CTAs write
   extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kHalves = halves_of(kTiles), kWarps = warps_of(kTiles);
   constexpr int kChunk = chunk_of(kTiles), kPitch = pitch_of(kTiles), kDepth = depth_of(kTiles);
   constexpr int kPerUnit = kUnit / kGroup;  // groups in a unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -132,7 +126,12 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, bl
   const int u0 = part * p.part_units;
   const int u1 = u0 + p.part_units < p.units ? u0 + p.part_units : p.units;
   const uint32_t sbase = smem_u32(smem);
+  // The next launch's blocks may take the places that this one's leave; they
+  // touch no memory before this grid is complete.
+  griddep_launch_dependents();
   griddep_wait();
+  // every CTA of the cluster is running before any writes into another's memory
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
   // inputs of units [u, u + kChunk / kUnit) into buffer `buf`; zero beyond the row's end
   auto stage_inputs = [&](int u, int buf) {
@@ -165,12 +164,13 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, bl
     uint32_t s[kHalves], z[kHalves];
   };
   // columns beyond the last block read the last one's weights and are not stored
-  const int block = tile * kWarps + warp < p.blocks ? tile * kWarps + warp : p.blocks - 1;
+  const int block_at = (tile * kTileN + warp * 16 * kHalves) / kBlockN, half0 = kHalves == 1 ? warp & 1 : 0;
+  const int block = block_at < p.blocks ? block_at : p.blocks - 1;
   const long long at = (long long)block * kRanks + rank;
   const long long group0 = at * p.groups + (long long)u0 * kPerUnit + q % kPerUnit;
-  const uint4* wp = p.weights + (at * p.units + u0) * 128 + lane;
-  const uint32_t* sp = p.scales + group0 * 16 + g;
-  const uint16_t* zp = kZeros ? p.zeros + group0 * 16 + g : nullptr;
+  const uint4* wp = p.weights + (at * p.units + u0) * 128 + half0 * 64 + lane;
+  const uint32_t* sp = p.scales + group0 * 16 + 8 * half0 + g;
+  const uint16_t* zp = kZeros ? p.zeros + group0 * 16 + 8 * half0 + g : nullptr;
   // unit `d` beyond the pointers
   auto fetch = [&](Unit& v, int d, bool in) {
     if (!in) return;
@@ -207,7 +207,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, bl
       if ((u - u0) % kChunkUnits == 0) {  // the chunk has arrived; the next one takes the other buffer
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        xu = sbase + (uint32_t)(buf * p.M * kPitch);
+        xu = (uint32_t)(buf * p.M * kPitch);
         buf ^= 1;
         if (u + kChunkUnits < u1) stage_inputs(u + kChunkUnits, buf);
       } else {
@@ -233,7 +233,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, bl
           const int h = grp * (kGroup / 32) + hh;
           uint4 xv[kTiles];
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) xv[t] = ld_shared_v4(xu + row[t] + 64u * h);
+          for (int t = 0; t < kTiles; ++t) xv[t] = *reinterpret_cast<const uint4*>(smem + xu + row[t] + 64 * h);
 #pragma unroll
           for (int b = 0; b < kHalves; ++b)
 #pragma unroll
@@ -269,8 +269,9 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, bl
       fetch(ring[d], d, u + kDepth < u1);  // into the registers just used
     }
   }
-  __syncthreads();  // every read of the inputs is done
-  float* sums = reinterpret_cast<float*>(smem);
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  // hand each CTA this rank's share of its columns
+  const uint32_t shares = sbase + (uint32_t)(2 * p.M * kPitch);
 #pragma unroll
   for (int b = 0; b < kHalves; ++b)
 #pragma unroll
@@ -278,24 +279,26 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * kWarps, bl
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int m = 8 * t + 2 * q + (i & 1);
-        if (m < p.M) sums[m * kTileN + (warp * kHalves + b) * 16 + g + 8 * (i >> 1)] = 64.f * acc[b][t][i];
+        const int col = (warp * kHalves + b) * 16 + g + 8 * (i >> 1);
+        if (m < p.M)
+          st_cluster_f32(mapa_shared(shares, col / kShare) +
+                             4u * (uint32_t)((rank * p.M + m) * kShare + col % kShare),
+                         64.f * acc[b][t][i]);
       }
-  cluster_sync();  // every rank's share is in its shared memory
+  cluster_sync();  // the shares of all ranks are here
 
-  // CTA r adds its kShare columns of the tile in rank order
-  const uint32_t mine = smem_u32(sums);
+  const float* share = reinterpret_cast<const float*>(smem + 2 * p.M * kPitch);
   for (int i = threadIdx.x; i < kShare * p.M; i += blockDim.x) {
-    const int m = i / kShare, col = rank * kShare + i % kShare;
-    const int n = tile * kTileN + col;
+    const int m = i / kShare;
+    const int n = tile * kTileN + rank * kShare + i % kShare;
     float s = 0.f;
 #pragma unroll
-    for (uint32_t r = 0; r < kRanks; ++r) s += ld_cluster_f32(mapa_shared(mine, r) + 4u * (m * kTileN + col));
+    for (int r = 0; r < kRanks; ++r) s += share[r * kShare * p.M + i];  // in rank order
     if (p.parts > 1)
       __stcg(p.partial + ((long long)part * p.M + m) * (gridDim.y * kTileN) + n, s);
     else if (n < p.N)
       p.out[(long long)m * p.N + n] = (uint16_t)(pack_bf16x2(s, 0.f) & 0xFFFFu);
   }
-  cluster_sync();  // no CTA leaves while its share is being read
   if (p.parts == 1) return;
 
   // the last part to arrive adds the parts in order
@@ -422,22 +425,30 @@ void split_of(const Layout& l, int64_t N, int* parts, int* part_units) {
 }
 
 template <int kTiles, int kGroup>
-void launch(const W4Params& p, dim3 grid, cudaStream_t st) {
-  const int inputs = 2 * p.M * pitch_of(kTiles), sums = p.M * kTileN * 4;
-  const int smem = inputs > sums ? inputs : sums;  // under 48 KB for every token count
-  if (p.zeros)
-    w4_kernel<kTiles, kGroup, true><<<grid, 32 * kWarps, smem, st>>>(p);
-  else
-    w4_kernel<kTiles, kGroup, false><<<grid, 32 * kWarps, smem, st>>>(p);
+int launch(const W4Params& p, dim3 grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * warps_of(kTiles));
+  // the inputs' two chunks and the ranks' shares: under 48 KB for every token count
+  cfg.dynamicSmemBytes = (size_t)(p.M * (2 * pitch_of(kTiles) + kRanks * kShare * 4));
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, p.zeros ? w4_kernel<kTiles, kGroup, true> : w4_kernel<kTiles, kGroup, false>, p) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_RS_ERR_CUDA;
+  }
+  return GEMM_RS_OK;
 }
 template <int kTiles>
-void launch(const W4Params& p, dim3 grid, cudaStream_t st) {
-  if (p.group == 32)
-    launch<kTiles, 32>(p, grid, st);
-  else if (p.group == 64)
-    launch<kTiles, 64>(p, grid, st);
-  else
-    launch<kTiles, 128>(p, grid, st);
+int launch(const W4Params& p, dim3 grid, cudaStream_t st) {
+  if (p.group == 32) return launch<kTiles, 32>(p, grid, st);
+  if (p.group == 64) return launch<kTiles, 64>(p, grid, st);
+  return launch<kTiles, 128>(p, grid, st);
 }
 
 }  // namespace
@@ -534,11 +545,8 @@ extern "C" int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int ha
   p.arrived = static_cast<uint32_t*>(workspace);
   p.partial = reinterpret_cast<float*>(p.arrived + tiles * kRanks);
   const dim3 grid(kRanks, (unsigned)tiles, (unsigned)p.parts);
-  if (M <= 8)
-    launch<1>(p, grid, st);
-  else if (M <= 16)
-    launch<2>(p, grid, st);
-  else
-    launch<4>(p, grid, st);
-  return launch_status();
+  if (M <= 8) return launch<1>(p, grid, st);
+  if (M <= 16) return launch<2>(p, grid, st);
+  if (M <= 24) return launch<3>(p, grid, st);
+  return launch<4>(p, grid, st);
 }
