@@ -120,12 +120,12 @@ int gemm_rs_bwd_destroy(gemm_rs_bwd_t plan);
  * four bits count); scales [8][ceil(K/8/group)][N] bf16; zeros of that shape,
  * bytes 0..127 (the low seven bits count), or NULL for 8 everywhere; out [M][N]
  * bf16.  Products are summed in fp32 in a fixed order and rounded once.
- * N % 8 == 0, at most 2^22; K % 64 == 0.
+ * N % 8 == 0, at most 2^19; K % 64 == 0.
  *
  * The weights are packed once into one buffer, whose contents are private to
  * this library; codes, scales and zeros are not needed after that. */
-int gemm_rs_w4_bytes(int64_t N, int64_t K, int group, int has_zeros, size_t* weight_bytes,
-                     size_t* workspace_bytes); /* host only */
+int gemm_rs_w4_bytes(int64_t N, int64_t K, int group, int has_zeros,
+                     size_t* weight_bytes); /* host only */
 /* Symmetric codes of W [8][K/8][N] bf16, rounded to nearest: scale =
  * bf16(largest magnitude of the group / 7), code = 8 + round(w / scale) in
  * 0..15; a group with an infinity or a NaN gets the scale NaN. */
@@ -133,11 +133,9 @@ int gemm_rs_w4_quantize(int64_t N, int64_t K, int group, const void* W, void* co
                         void* stream);
 int gemm_rs_w4_pack(int64_t N, int64_t K, int group, const void* codes, const void* scales,
                     const void* zeros, void* weight, void* stream);
-/* workspace: workspace_bytes (of any has_zeros), all zero before the first
- * call; every call leaves its control words zero again.  Calls that can overlap
- * on the GPU need workspaces of their own. */
+/* Needs no workspace. */
 int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int has_zeros, const void* x,
-                   const void* weight, void* out, void* workspace, void* stream);
+                   const void* weight, void* out, void* stream);
 
 #ifdef __cplusplus
 }

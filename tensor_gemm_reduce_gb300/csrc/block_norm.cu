@@ -1,7 +1,6 @@
 // block_norm.cu -- the norms after and before a block, fused with the block's
 // gate and residual scale, forward and backward (gemm_rs_norm_* in
 // include/gemm_rs_ops.h).
-#include <atomic>
 #include <cmath>
 
 #include "ops_common.cuh"
@@ -653,20 +652,10 @@ void set_shape(NormParams* p, const Shape& s) {
   p->stages = s.stages;
 }
 
-// Launches Kernel, with more than 48 KB of shared memory allowed once for each device.
 template <auto Kernel, typename... Args>
 int launch(int grid, int threads, int smem, cudaStream_t st, Args... args) {
-  static std::atomic<uint64_t> allowed{0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
-    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_RS_ERR_CUDA;
-    }
-    allowed.fetch_or(bit, std::memory_order_relaxed);
-  }
+  static SmemAllowed allowed;
+  if (!allowed.set(Kernel, kMaxSmem)) return GEMM_RS_ERR_CUDA;
   Kernel<<<grid, threads, smem, st>>>(args...);
   return launch_status();
 }

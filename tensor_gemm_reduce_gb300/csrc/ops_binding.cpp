@@ -235,23 +235,22 @@ PyObject* backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// x, N, K, group, has_zeros, packed weight, out, workspace, stream
+// x, N, K, group, has_zeros, packed weight, out, stream
 PyObject* w4_matvec(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 9, [&] {
+  return guarded(n, 8, [&] {
     Call c;
     const at::Tensor& t = c.tensor(a[0], "x");
     const int64_t N = PyLong_AsLongLong(a[1]), K = PyLong_AsLongLong(a[2]);
     const int group = (int)PyLong_AsLong(a[3]), zeros = PyObject_IsTrue(a[4]) == 1;
-    size_t weight_bytes = 0, need = 0;
-    const int rc = gemm_rs_w4_bytes(N, K, group, zeros, &weight_bytes, &need);
+    size_t weight_bytes = 0;
+    const int rc = gemm_rs_w4_bytes(N, K, group, zeros, &weight_bytes);
     if (rc) return rc;
     if (t.dim() != 3) value_error("x must have shape [8][M][K/8], got " + text(t.sizes()));
     const int64_t M = t.size(1), xs[3] = {kWorld, M, K / kWorld}, os[2] = {M, N};
     void* x = c.in(a[0], kB, xs, "x");
     void* w = c.buffer(a[5], weight_bytes, "weight", false);
     void* out = c.out(a[6], kB, os, "out");
-    void* ws = c.buffer(a[7], need, "workspace", true);
-    return gemm_rs_w4_run(M, N, K, group, zeros, x, w, out, ws, c.stream(a[8]));
+    return gemm_rs_w4_run(M, N, K, group, zeros, x, w, out, c.stream(a[7]));
   });
 }
 

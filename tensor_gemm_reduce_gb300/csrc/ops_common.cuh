@@ -40,6 +40,28 @@ inline int launch_status() {
   return cudaGetLastError() == cudaSuccess ? GEMM_RS_OK : GEMM_RS_ERR_CUDA;
 }
 
+// More than 48 KB of dynamic shared memory for a kernel, asked for once on each
+// device.
+class SmemAllowed {
+ public:
+  template <typename Kernel>
+  bool set(Kernel kernel, int bytes) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done_.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    done_.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
+
 inline bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {

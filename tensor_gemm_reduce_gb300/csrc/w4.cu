@@ -18,9 +18,11 @@
 // group's sum is scaled in fp32 and added to the total, which takes 2^6 at the end.  The masks
 // and shifts keep the integer pipe the busiest: 5 instructions for 8 weights.
 //
-// Split: a cluster of 8 CTAs computes 128 columns, CTA r rank r's share of the
-// sum; the eight fp32 partial sums are exchanged through distributed shared
-// memory and CTA r writes an eighth of the columns, added in rank order: the layer's reduce-scatter, inside one cluster.
+// Split: a cluster of 8 CTAs computes up to 128 columns, CTA r rank r's share of
+// the sum; each CTA hands the others their columns of its share through
+// distributed shared memory and adds the eight (in rank order) that it is handed:
+// the layer's reduce-scatter, inside one cluster.  Inside a CTA the warps take
+// columns, and where there are few columns also parts of the inner dimension.
 #include "ops_common.cuh"
 
 using namespace grs;
@@ -29,26 +31,20 @@ namespace {
 
 constexpr int kRanks = 8;
 constexpr int kBlockN = 32;         // columns that lie together in the packed weights, in two halves
-constexpr int kTileN = 4 * kBlockN; // columns of a cluster
-constexpr int kShare = kTileN / kRanks;  // columns that a CTA of the cluster writes
 constexpr int kCell = 64;           // inner elements of a lane's 16-byte load
 constexpr int kUnit = 128;          // inner elements of a step: two cells of each half
 constexpr int kMaxTokens = 32;
-constexpr int kMaxParts = 8;
+constexpr int kMaxSmem = 227 * 1024;
+// Warps that an SM holds at 128 registers a thread, and that run at once on the
+// 148 SMs that clusters of 8 CTAs reach.
+constexpr int kSmWarps = 16;
+constexpr int kRunningWarps = kSmWarps * 148;
 
-// Inner elements of a chunk of the inputs in shared memory, for `tiles` tiles
-// of 8 tokens, and its row pitch in bytes (64 beyond a multiple of 128, so that
-// the two rows that 8 lanes read lie in different banks).
-__host__ __device__ constexpr int chunk_of(int tiles) { return tiles > 2 ? 128 : 1024 / tiles; }
-__host__ __device__ constexpr int pitch_of(int tiles) { return 2 * chunk_of(tiles) + 64; }
 // Halves of a block that a warp multiplies (one set of input fragments serves
-// both, but 3 and 4 token tiles leave no registers for a second one), warps of a
-// CTA, units of weights in flight for each warp, and CTAs that share an SM: at 4
-// (2 of twice the warps) the 512 CTAs of 8192 columns all run at once.
+// both, but 3 and 4 token tiles leave no registers for a second one), and units
+// of weights in flight for each warp.
 __host__ __device__ constexpr int halves_of(int tiles) { return tiles <= 2 ? 2 : 1; }
-__host__ __device__ constexpr int warps_of(int tiles) { return kTileN / 16 / halves_of(tiles); }
-__host__ __device__ constexpr int depth_of(int tiles) { return tiles <= 2 ? 3 : 4; }
-__host__ __device__ constexpr int ctas_of(int tiles) { return 16 / warps_of(tiles); }
+__host__ __device__ constexpr int depth_of(int tiles) { return tiles == 1 ? 3 : tiles == 2 ? 2 : 4; }
 
 // Packed buffer: weights [N/32][8][units][2 halves][2 cells][32 lanes] of 16
 // bytes, then scales [N/32][8][groups][2 halves][8] of two bf16 (columns g and
@@ -78,14 +74,14 @@ Layout layout_of(int64_t N, int64_t K, int group, bool zeros) {
 struct W4Params {
   int M, N, Kr, group;
   int blocks, units, groups;   // units and groups of a rank
-  int parts, part_units;       // the units of a rank are cut into parts of part_units
+  int wn, wk;                  // warps of a CTA: wn of columns x wk parts of the units
+  int part_units;              // units of a part
+  int chunks, chunk_units, pitch;  // a part's inputs arrive in chunks: units, row pitch in bytes
   const uint16_t* x;           // [8][M][Kr]
   const uint4* weights;
   const uint32_t* scales;
   const uint16_t* zeros;
   uint16_t* out;               // [M][N]
-  float* partial;              // parts > 1: [parts][M][tiles * 128]
-  uint32_t* arrived;           // parts > 1: one count for each CTA of a cluster
 };
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -112,20 +108,23 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
 
 // kTiles tiles of 8 tokens, groups of kGroup inner elements.
 template <int kTiles, int kGroup, bool kZeros>
-__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * warps_of(kTiles), ctas_of(kTiles))
+__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(256, 2)
     w4_kernel(const W4Params p) {
-  // two chunks of the inputs [token][chunk], then the ranks' shares of this CTA's
-  // columns [rank][token][kShare], which their CTAs write
+  // for each part two chunks of the inputs [token][chunk]; then the ranks' and
+  // parts' shares of this CTA's columns [rank][part][token][column], which the
+  // cluster's CTAs write
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kHalves = halves_of(kTiles), kWarps = warps_of(kTiles);
-  constexpr int kChunk = chunk_of(kTiles), kPitch = pitch_of(kTiles), kDepth = depth_of(kTiles);
+  constexpr int kHalves = halves_of(kTiles), kDepth = depth_of(kTiles);
   constexpr int kPerUnit = kUnit / kGroup;  // groups in a unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x, tile = blockIdx.y, part = blockIdx.z;
+  const int part = warp / p.wn, wn = warp - part * p.wn;
+  const int rank = blockIdx.x, tile = blockIdx.y;
   const int g = lane >> 2, q = lane & 3;
-  const int u0 = part * p.part_units;
+  const int cols = 16 * kHalves * p.wn, share = cols / kRanks;  // of the cluster, of a CTA
+  const int u0 = part * p.part_units < p.units ? part * p.part_units : p.units;
   const int u1 = u0 + p.part_units < p.units ? u0 + p.part_units : p.units;
   const uint32_t sbase = smem_u32(smem);
+  const uint32_t inputs = (uint32_t)(part * 2 * p.M * p.pitch);  // this part's chunks
   // The next launch's blocks may take the places that this one's leave; they
   // touch no memory before this grid is complete.
   griddep_launch_dependents();
@@ -133,18 +132,19 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * warps_of(k
   // every CTA of the cluster is running before any writes into another's memory
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
-  // inputs of units [u, u + kChunk / kUnit) into buffer `buf`; zero beyond the row's end
+  // inputs of units [u, u + chunk_units) into buffer `buf`; zero beyond the row's end
   auto stage_inputs = [&](int u, int buf) {
-    const int k0 = u * kUnit;
-    const int vectors = (u1 - u) * kUnit < kChunk ? (u1 - u) * (kUnit / 8) : kChunk / 8;
-    for (int i = threadIdx.x; i < p.M * vectors; i += blockDim.x) {
-      const int m = i / vectors, k = (i - m * vectors) * 8;
-      const uint32_t dst = sbase + (uint32_t)((buf * p.M + m) * kPitch + 2 * k);
-      const uint16_t* src = p.x + ((long long)rank * p.M + m) * p.Kr + k0 + k;
-      const bool in = k0 + k < p.Kr;
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(in ? src : p.x),
-                   "r"(in ? 16 : 0)
-                   : "memory");
+    const int vectors = (u1 - u < p.chunk_units ? u1 - u : p.chunk_units) * (kUnit / 8);
+    for (int m = wn; m < p.M; m += p.wn) {
+      const uint16_t* src = p.x + ((long long)rank * p.M + m) * p.Kr;
+      for (int v = lane; v < vectors; v += 32) {
+        const int k = u * kUnit + 8 * v;
+        const bool in = k < p.Kr;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         sbase + inputs + (uint32_t)((buf * p.M + m) * p.pitch + 16 * v)),
+                     "l"(in ? src + k : p.x), "r"(in ? 16 : 0)
+                     : "memory");
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -164,7 +164,8 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * warps_of(k
     uint32_t s[kHalves], z[kHalves];
   };
   // columns beyond the last block read the last one's weights and are not stored
-  const int block_at = (tile * kTileN + warp * 16 * kHalves) / kBlockN, half0 = kHalves == 1 ? warp & 1 : 0;
+  const int half_at = tile * (p.wn * kHalves) + wn * kHalves;  // this warp's first half of a block
+  const int block_at = half_at / 2, half0 = half_at % 2;
   const int block = block_at < p.blocks ? block_at : p.blocks - 1;
   const long long at = (long long)block * kRanks + rank;
   const long long group0 = at * p.groups + (long long)u0 * kPerUnit + q % kPerUnit;
@@ -185,16 +186,16 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * warps_of(k
   Unit ring[kDepth];
 #pragma unroll
   for (int d = 0; d < kDepth; ++d) fetch(ring[d], d, u0 + d < u1);
-  stage_inputs(u0, 0);
+  if (u0 < u1) stage_inputs(u0, 0);
 
   // tokens beyond the last read its row; their columns are not stored
   uint32_t row[kTiles];
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) row[t] = (uint32_t)((8 * t + g < p.M ? 8 * t + g : p.M - 1) * kPitch + 16 * q);
+  for (int t = 0; t < kTiles; ++t) row[t] = (uint32_t)((8 * t + g < p.M ? 8 * t + g : p.M - 1) * p.pitch + 16 * q);
 
   int buf = 0;
   uint32_t xu = 0;  // the unit's inputs
-  constexpr int kChunkUnits = kChunk / kUnit;
+  int chunk_end = u0, synced = 0;
 #pragma unroll 1
   for (int base = u0; base < u1; base += kDepth) {
     wp += kDepth * 128;
@@ -204,12 +205,14 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * warps_of(k
     for (int d = 0; d < kDepth; ++d) {
       const int u = base + d;
       if (u >= u1) break;
-      if ((u - u0) % kChunkUnits == 0) {  // the chunk has arrived; the next one takes the other buffer
+      if (u == chunk_end) {  // the chunk has arrived; the next one takes the other buffer
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        xu = (uint32_t)(buf * p.M * kPitch);
+        ++synced;
+        xu = inputs + (uint32_t)(buf * p.M * p.pitch);
         buf ^= 1;
-        if (u + kChunkUnits < u1) stage_inputs(u + kChunkUnits, buf);
+        chunk_end += p.chunk_units;
+        if (chunk_end < u1) stage_inputs(chunk_end, buf);
       } else {
         xu += 2 * kUnit;
       }
@@ -269,9 +272,13 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * warps_of(k
       fetch(ring[d], d, u + kDepth < u1);  // into the registers just used
     }
   }
+  // A shorter last part keeps the others company at their chunks' barriers.  (One
+  // barrier for each part would do, but a kernel that names barriers at run time
+  // holds all 16 of a CTA, and an SM has 64: no more than 4 CTAs.)
+  for (; synced < p.chunks; ++synced) __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  // hand each CTA this rank's share of its columns
-  const uint32_t shares = sbase + (uint32_t)(2 * p.M * kPitch);
+  // hand each CTA this warp's sums for its columns
+  const uint32_t shares = (uint32_t)(p.wk * 2 * p.M * p.pitch);
 #pragma unroll
   for (int b = 0; b < kHalves; ++b)
 #pragma unroll
@@ -279,46 +286,23 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(32 * warps_of(k
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int m = 8 * t + 2 * q + (i & 1);
-        const int col = (warp * kHalves + b) * 16 + g + 8 * (i >> 1);
+        const int col = (wn * kHalves + b) * 16 + g + 8 * (i >> 1), owner = col / share;
         if (m < p.M)
-          st_cluster_f32(mapa_shared(shares, col / kShare) +
-                             4u * (uint32_t)((rank * p.M + m) * kShare + col % kShare),
+          st_cluster_f32(mapa_shared(sbase + shares, owner) +
+                             4u * (uint32_t)(((rank * p.wk + part) * p.M + m) * share + col - owner * share),
                          64.f * acc[b][t][i]);
       }
   cluster_sync();  // the shares of all ranks are here
 
-  const float* share = reinterpret_cast<const float*>(smem + 2 * p.M * kPitch);
-  for (int i = threadIdx.x; i < kShare * p.M; i += blockDim.x) {
-    const int m = i / kShare;
-    const int n = tile * kTileN + rank * kShare + i % kShare;
-    float s = 0.f;
-#pragma unroll
-    for (int r = 0; r < kRanks; ++r) s += share[r * kShare * p.M + i];  // in rank order
-    if (p.parts > 1)
-      __stcg(p.partial + ((long long)part * p.M + m) * (gridDim.y * kTileN) + n, s);
-    else if (n < p.N)
-      p.out[(long long)m * p.N + n] = (uint16_t)(pack_bf16x2(s, 0.f) & 0xFFFFu);
-  }
-  if (p.parts == 1) return;
-
-  // the last part to arrive adds the parts in order
-  __shared__ uint32_t last;
-  __threadfence();
-  __syncthreads();
-  uint32_t* count = p.arrived + tile * kRanks + rank;
-  if (threadIdx.x == 0) last = atomicAdd(count, 1u) == (uint32_t)p.parts - 1u;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  for (int i = threadIdx.x; i < kShare * p.M; i += blockDim.x) {
-    const int m = i / kShare, n = tile * kTileN + rank * kShare + i % kShare;
+  const float* from = reinterpret_cast<const float*>(smem + shares);
+  for (int i = threadIdx.x; i < share * p.M; i += blockDim.x) {
+    const int m = i / share;
+    const int n = tile * cols + rank * share + (i - m * share);
     if (n >= p.N) continue;
     float s = 0.f;
-    for (int z = 0; z < p.parts; ++z)
-      s += __ldcg(p.partial + ((long long)z * p.M + m) * (gridDim.y * kTileN) + n);
+    for (int r = 0; r < kRanks * p.wk; ++r) s += from[r * share * p.M + i];  // in order
     p.out[(long long)m * p.N + n] = (uint16_t)(pack_bf16x2(s, 0.f) & 0xFFFFu);
   }
-  if (threadIdx.x == 0) *count = 0;  // ready for the next call
 }
 
 struct PackParams {
@@ -405,66 +389,79 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const uint16_t* W, uin
 
 int check(int64_t M, int64_t N, int64_t K, int group) {
   if (group != 32 && group != 64 && group != 128) return GEMM_RS_ERR_INVALID_ARG;
-  if (M < 0 || M > kMaxTokens || N < 0 || K < 0 || N % 8 || K % 64 || N > (1ll << 22) || K > (1ll << 30))
+  if (M < 0 || M > kMaxTokens || N < 0 || K < 0 || N % 8 || K % 64 || N > (1ll << 19) || K > (1ll << 30))
     return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
   return GEMM_RS_OK;
 }
 
-// Few columns leave SMs idle: the inner dimension is then cut into parts.
-void split_of(const Layout& l, int64_t N, int* parts, int* part_units) {
-  const long long ctas = (N + kTileN - 1) / kTileN * kRanks;
-  long long want = ctas > 0 ? 304 / ctas : 1;
-  const long long units = l.units;
-  if (want > kMaxParts) want = kMaxParts;
-  if (want > units / 4) want = units / 4;  // at least 4 units (8 KiB a warp) in a part
-  if (want < 1) want = 1;
-  const long long per = (units + want - 1) / want;
-  *part_units = (int)per;
-  *parts = (int)(per > 0 ? (units + per - 1) / per : 1);
-  if (*parts < 1) *parts = 1;
+// How the columns and the inner dimension are cut: clusters of 128 columns, and
+// fewer columns where that leaves under 32 clusters (256 CTAs); then as many
+// parts of the inner dimension as fill the warps that can run at once.
+// One token, us: 1024 columns, K = 28672: 16 columns x 8 parts 6.8, 64 x 2 11.0,
+// 128 x 1 15; 4096 columns, K = 8192: 128 x 2 6.9, 128 x 1 8.5; at 8192 columns
+// 128 x 1 9.6, 64 x 2 12.1.  (Narrower clusters for an even load of the SMs gained
+// nothing at 8192 columns: 112 columns on 148 SMs as long as 128 on 128.)
+struct Split {
+  int wn, wk, clusters, part_units, chunk_units, pitch, smem;
+};
+Split split_of(int64_t M, int64_t N, int units, int tiles) {
+  Split s = {};
+  const int half_cols = 16 * halves_of(tiles);
+  s.wn = 128 / half_cols;
+  while (s.wn > 1 && N <= 31ll * half_cols * s.wn) s.wn /= 2;
+  s.clusters = (int)((N + half_cols * s.wn - 1) / (half_cols * s.wn));
+  s.wk = kRunningWarps / (s.clusters * kRanks * s.wn);
+  if (s.wk > 8 / s.wn) s.wk = 8 / s.wn;
+  if (s.wk > units) s.wk = units;
+  if (s.wk < 1) s.wk = 1;
+  s.part_units = (units + s.wk - 1) / s.wk;
+  s.wk = (units + s.part_units - 1) / s.part_units;
+  // the inputs' chunks: up to 8 units, an even number (a warp copies two at a time),
+  // within the shared memory of as many CTAs as an SM's registers hold
+  const int room = kMaxSmem / (kSmWarps / (s.wn * s.wk)) - 2 * 1024;
+  for (int most = s.part_units < 8 ? s.part_units : 8;; most = most > 2 ? (most - 1) / 2 * 2 : 1) {
+    s.chunk_units = most;
+    s.pitch = s.chunk_units * kUnit * 2 + 64;  // two rows that 8 lanes read lie in different banks
+    s.smem = (int)(s.wk * M * (2 * s.pitch + half_cols * s.wn * 4));  // and the shares
+    if (most == 1 || s.smem <= room) return s;
+  }
 }
 
 template <int kTiles, int kGroup>
-int launch(const W4Params& p, dim3 grid, cudaStream_t st) {
+int launch(const W4Params& p, const Split& sp, cudaStream_t st) {
+  const auto kernel = p.zeros ? w4_kernel<kTiles, kGroup, true> : w4_kernel<kTiles, kGroup, false>;
+  static SmemAllowed allowed[2];
+  if (!allowed[p.zeros != nullptr].set(kernel, kMaxSmem)) return GEMM_RS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(32 * warps_of(kTiles));
-  // the inputs' two chunks and the ranks' shares: under 48 KB for every token count
-  cfg.dynamicSmemBytes = (size_t)(p.M * (2 * pitch_of(kTiles) + kRanks * kShare * 4));
+  cfg.gridDim = dim3(kRanks, (unsigned)sp.clusters);
+  cfg.blockDim = dim3(32 * sp.wn * sp.wk);
+  cfg.dynamicSmemBytes = (size_t)sp.smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, p.zeros ? w4_kernel<kTiles, kGroup, true> : w4_kernel<kTiles, kGroup, false>, p) !=
-      cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_RS_ERR_CUDA;
   }
   return GEMM_RS_OK;
 }
 template <int kTiles>
-int launch(const W4Params& p, dim3 grid, cudaStream_t st) {
-  if (p.group == 32) return launch<kTiles, 32>(p, grid, st);
-  if (p.group == 64) return launch<kTiles, 64>(p, grid, st);
-  return launch<kTiles, 128>(p, grid, st);
+int launch(const W4Params& p, const Split& sp, cudaStream_t st) {
+  if (p.group == 32) return launch<kTiles, 32>(p, sp, st);
+  if (p.group == 64) return launch<kTiles, 64>(p, sp, st);
+  return launch<kTiles, 128>(p, sp, st);
 }
 
 }  // namespace
 
-extern "C" int gemm_rs_w4_bytes(int64_t N, int64_t K, int group, int has_zeros, size_t* weight_bytes,
-                                size_t* workspace_bytes) {
+extern "C" int gemm_rs_w4_bytes(int64_t N, int64_t K, int group, int has_zeros, size_t* weight_bytes) {
   const int rc = check(0, N, K, group);
   if (rc) return rc;
-  const Layout l = layout_of(N, K, group, has_zeros != 0);
-  if (weight_bytes) *weight_bytes = (size_t)l.bytes;
-  if (workspace_bytes) {
-    int parts = 1, part_units = 0;
-    split_of(l, N, &parts, &part_units);
-    const size_t tiles = (size_t)(N + kTileN - 1) / kTileN;
-    *workspace_bytes = tiles * kRanks * 4 + (parts > 1 ? (size_t)parts * kMaxTokens * tiles * kTileN * 4 : 0);
-  }
+  if (!weight_bytes) return GEMM_RS_ERR_INVALID_ARG;
+  *weight_bytes = (size_t)layout_of(N, K, group, has_zeros != 0).bytes;
   return GEMM_RS_OK;
 }
 
@@ -508,13 +505,12 @@ extern "C" int gemm_rs_w4_pack(int64_t N, int64_t K, int group, const void* code
 }
 
 extern "C" int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int has_zeros, const void* x,
-                              const void* weight, void* out, void* workspace, void* stream) {
+                              const void* weight, void* out, void* stream) {
   int rc = check(M, N, K, group);
   if (rc) return rc;
   if (M == 0 || N == 0) return GEMM_RS_OK;
   if (!out || (K > 0 && (!x || !weight))) return GEMM_RS_ERR_INVALID_ARG;
-  if (!workspace) return GEMM_RS_ERR_WORKSPACE;
-  for (const void* q : {x, weight, (const void*)out, (const void*)workspace})
+  for (const void* q : {x, weight, (const void*)out})
     if (misaligned16(q)) return GEMM_RS_ERR_MISALIGNED;
   int sms = 0;
   rc = current_device_sms(&sms);
@@ -527,7 +523,6 @@ extern "C" int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int ha
   }
   const Layout l = layout_of(N, K, group, has_zeros != 0);
   const uint8_t* base = static_cast<const uint8_t*>(weight);
-  const int tiles = (int)((N + kTileN - 1) / kTileN);
   W4Params p;
   p.M = (int)M;
   p.N = (int)N;
@@ -536,17 +531,23 @@ extern "C" int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int ha
   p.blocks = (int)l.blocks;
   p.groups = (int)l.groups;
   p.units = (int)l.units;
-  split_of(l, N, &p.parts, &p.part_units);
+  const int tiles = (int)((M + 7) / 8);
+  const Split sp = split_of(M, N, p.units, tiles);
+  p.wn = sp.wn;
+  p.wk = sp.wk;
+  p.part_units = sp.part_units;
+  p.chunk_units = sp.chunk_units;
+  p.chunks = (sp.part_units + sp.chunk_units - 1) / sp.chunk_units;
+  p.pitch = sp.pitch;
   p.x = static_cast<const uint16_t*>(x);
   p.weights = reinterpret_cast<const uint4*>(base);
   p.scales = reinterpret_cast<const uint32_t*>(base + l.scale_off);
   p.zeros = has_zeros ? reinterpret_cast<const uint16_t*>(base + l.zero_off) : nullptr;
   p.out = static_cast<uint16_t*>(out);
-  p.arrived = static_cast<uint32_t*>(workspace);
-  p.partial = reinterpret_cast<float*>(p.arrived + tiles * kRanks);
-  const dim3 grid(kRanks, (unsigned)tiles, (unsigned)p.parts);
-  if (M <= 8) return launch<1>(p, grid, st);
-  if (M <= 16) return launch<2>(p, grid, st);
-  if (M <= 24) return launch<3>(p, grid, st);
-  return launch<4>(p, grid, st);
+  switch (tiles) {
+    case 1: return launch<1>(p, sp, st);
+    case 2: return launch<2>(p, sp, st);
+    case 3: return launch<3>(p, sp, st);
+    default: return launch<4>(p, sp, st);
+  }
 }

@@ -46,10 +46,10 @@ SIGS = {
     "gemm_rs_bwd_run": [_P] * 9,
     "gemm_rs_bwd_status": [_P, _P],
     "gemm_rs_bwd_destroy": [_P],
-    "gemm_rs_w4_bytes": [_L, _L, _I, _I, _P, _P],
+    "gemm_rs_w4_bytes": [_L, _L, _I, _I, _P],
     "gemm_rs_w4_quantize": [_L, _L, _I, _P, _P, _P, _P],
     "gemm_rs_w4_pack": [_L, _L, _I, _P, _P, _P, _P, _P],
-    "gemm_rs_w4_run": [_L, _L, _L, _I, _I, _P, _P, _P, _P, _P],
+    "gemm_rs_w4_run": [_L, _L, _L, _I, _I, _P, _P, _P, _P],
 }
 
 _LIB: Optional[ctypes.CDLL] = None

@@ -2,7 +2,7 @@
 scales (binding of gemm_rs_w4_* in include/gemm_rs_ops.h).
 
     weight = w4.pack(codes, scales, zeros, group=128)     once
-    out = w4.matvec(x, weight, workspace=w4.new_workspace(weight))
+    out = w4.matvec(x, weight)
 
     out[m][n] = sum_r sum_k x[r][m][k] (codes[r][k][n] - zeros[r][k//group][n]) scales[r][k//group][n]
 
@@ -27,10 +27,9 @@ class Weight:
 
     def __init__(self, N: int, K: int, group: int, has_zeros: bool, device=None):
         self.N, self.K, self.group, self.has_zeros = int(N), int(K), int(group), bool(has_zeros)
-        n, ws = ctypes.c_size_t(), ctypes.c_size_t()
-        _a.check(_a.lib().gemm_rs_w4_bytes(self.N, self.K, self.group, self.has_zeros, ctypes.byref(n),
-                                           ctypes.byref(ws)), "gemm_rs_w4_bytes")
-        self.workspace_bytes = ws.value
+        n = ctypes.c_size_t()
+        _a.check(_a.lib().gemm_rs_w4_bytes(self.N, self.K, self.group, self.has_zeros, ctypes.byref(n)),
+                 "gemm_rs_w4_bytes")
         device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
         self.data = torch.empty(n.value, dtype=_U8, device=device)
 
@@ -69,8 +68,9 @@ def pack(codes, scales, zeros=None, group: int = 128, stream=None) -> Weight:
 
 
 def new_workspace(weight: Weight):
-    """Zeroed workspace of matvec(); calls that may overlap on the GPU need one each."""
-    return torch.zeros(max(weight.workspace_bytes, 16), dtype=_U8, device=weight.data.device)
+    """Workspace of matvec(): empty, its sums meet in the SMs' shared memory.  It is
+    there so that callers can treat this layer like the library's others."""
+    return torch.empty(0, dtype=_U8, device=weight.data.device)
 
 
 def matvec(x, weight: Weight, out=None, workspace=None, stream=None):
@@ -79,9 +79,7 @@ def matvec(x, weight: Weight, out=None, workspace=None, stream=None):
         if x.dim() != 3:
             raise ValueError(f"x must have shape [{_a.WORLD}][M][K/{_a.WORLD}], got {tuple(x.shape)}")
         out = torch.empty(x.shape[1], weight.N, dtype=_BF16, device=x.device)
-    if workspace is None:
-        workspace = new_workspace(weight)
-    rc = _a.ops().w4_matvec(x, weight.N, weight.K, weight.group, weight.has_zeros, weight.data, out, workspace,
+    rc = _a.ops().w4_matvec(x, weight.N, weight.K, weight.group, weight.has_zeros, weight.data, out,
                             None if stream is None else stream.cuda_stream)
     if rc:
         _a.check(rc, "gemm_rs_w4_run")
