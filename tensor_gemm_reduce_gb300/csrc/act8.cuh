@@ -17,6 +17,16 @@ inline int64_t act8_pitch(int64_t cols) { return (cols + 127) / 128 * 128; }
 // (only read beyond the rows and columns there are) gives 0.
 __device__ __forceinline__ uint32_t act8_scale2(uint32_t b) { return (b << 7) * 0x10001u; }
 
+// Two magnitudes times `inv2` (a power of two, at most 127 as products), rounded
+// to nearest even, as 0x4300 | m.
+__device__ __forceinline__ uint32_t act8_round2(uint32_t mag, uint32_t inv2) {
+  const uint32_t k128 = 0x43004300u;
+  const __nv_bfloat162 r =
+      __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&mag), *reinterpret_cast<const __nv_bfloat162*>(&inv2),
+              *reinterpret_cast<const __nv_bfloat162*>(&k128));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // Four code bytes to four bf16, elements 0, 1 in .x and 2, 3 in .y:
 // (128 + m) - 128 and the product with a power of two are exact in bf16.
 __device__ __forceinline__ uint32_t act8_magnitude2(uint32_t m, uint32_t scale2) {

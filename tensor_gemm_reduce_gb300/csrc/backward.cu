@@ -508,21 +508,7 @@ extern "C" int gemm_rs_bwd_run(gemm_rs_bwd_t h, const void* dY, const void* W, c
   if (!ok) return GEMM_RS_ERR_CUDA;
   p.s = schedule_of(da ? product_of(h->M, h->Kr, h->N) : none, dw ? product_of(h->Kr, h->N, h->M) : none,
                     h->max_pairs);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2u * (unsigned)p.s.pairs);
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.dynamicSmemBytes = kSmemAlloc;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, backward_kernel, p) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_RS_ERR_CUDA;
-  }
-  return GEMM_RS_OK;
+  return launch_overlapped(backward_kernel, dim3(2u * (unsigned)p.s.pairs), 32 * kWarps, kSmemAlloc, st, p);
 }
 
 extern "C" int gemm_rs_bwd_status(gemm_rs_bwd_t h, void* stream) {

@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
   const uint32_t c = blockIdx.x * p.groups + group, step = p.step;
   const uint32_t m0 = step == 1 ? c * p.chunk_rows : c;
   const uint32_t m1 = step == 1 && m0 + p.chunk_rows < p.M ? m0 + p.chunk_rows : p.M;
+  griddep_launch_dependents();  // the next launch's blocks take the places that free up, and wait
   griddep_wait();
 
   auto fetch = [&](uint32_t row, int stage) {
@@ -367,6 +368,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   const uint32_t step = kMode == kSequence ? 1 : p.step;
   const uint32_t m0 = step == 1 ? (c * p.chunk_rows < p.M ? c * p.chunk_rows : p.M) : c;
   const uint32_t m1 = step == 1 && m0 + p.chunk_rows < p.M ? m0 + p.chunk_rows : p.M;
+  griddep_launch_dependents();  // the next launch's blocks take the places that free up, and wait
   griddep_wait();
 
   auto fetch = [&](uint32_t row, int stage) {
@@ -517,7 +519,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
     fetch(m + p.stages * step, stage);  // every read of the slot is done
     if (++stage == p.stages) stage = 0;
   }
-  griddep_launch_dependents();
 
   // add the block's groups; the ring is free once every thread is here
   if (kMode == kSequence)
@@ -556,6 +557,7 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const NormParams p, int 
   const int col = blockIdx.x * 32 + lane;
   const bool in = col < p.D;
   const int job = blockIdx.y;
+  griddep_launch_dependents();
   griddep_wait();
   const float* src;
   int n = p.blocks;  // rows of src to add, `step` apart
@@ -652,26 +654,25 @@ void set_shape(NormParams* p, const Shape& s) {
   p->stages = s.stages;
 }
 
-template <auto Kernel, typename... Args>
-int launch(int grid, int threads, int smem, cudaStream_t st, Args... args) {
+template <auto Kernel>
+int launch(const NormParams& p, int grid, int threads, int smem, cudaStream_t st) {
   static SmemAllowed allowed;
   if (!allowed.set(Kernel, kMaxSmem)) return GEMM_RS_ERR_CUDA;
-  Kernel<<<grid, threads, smem, st>>>(args...);
-  return launch_status();
+  return launch_overlapped(Kernel, dim3((unsigned)grid), threads, (size_t)smem, st, p);
 }
 
 template <int V>
 int launch_forward(const NormParams& p, bool gate_ring, int grid, int smem, cudaStream_t st) {
   const int threads = 32 * p.warps * p.groups;
-  return gate_ring ? launch<norm_forward_kernel<V, true>>(grid, threads, smem, st, p)
-                    : launch<norm_forward_kernel<V, false>>(grid, threads, smem, st, p);
+  return gate_ring ? launch<norm_forward_kernel<V, true>>(p, grid, threads, smem, st)
+                    : launch<norm_forward_kernel<V, false>>(p, grid, threads, smem, st);
 }
 template <int V>
 int launch_backward(const NormParams& p, GateMode mode, int smem, cudaStream_t st) {
   const int threads = 32 * p.warps * p.groups;
-  if (mode == kSingle) return launch<norm_backward_kernel<V, kSingle>>(p.blocks, threads, smem, st, p);
-  if (mode == kSequence) return launch<norm_backward_kernel<V, kSequence>>(p.blocks, threads, smem, st, p);
-  return launch<norm_backward_kernel<V, kElement>>(p.blocks, threads, smem, st, p);
+  if (mode == kSingle) return launch<norm_backward_kernel<V, kSingle>>(p, p.blocks, threads, smem, st);
+  if (mode == kSequence) return launch<norm_backward_kernel<V, kSequence>>(p, p.blocks, threads, smem, st);
+  return launch<norm_backward_kernel<V, kElement>>(p, p.blocks, threads, smem, st);
 }
 
 const uint4* in(const void* p) { return static_cast<const uint4*>(p); }
@@ -781,18 +782,6 @@ extern "C" int gemm_rs_norm_backward(const gemm_rs_norm_desc* d, const void* dr,
   if (rc) return rc;
   const int many_gates = mode != kSingle, by_gate = d->gate_rows < sp.chunks;
   const long long crossing = mode != kSequence ? 0 : by_gate ? d->gate_rows : sp.chunks - 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.D + 31) / 32), (unsigned)(2 + crossing));
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];  // its blocks start while the last rows are worked on, and wait
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, norm_join_kernel, (const NormParams&)p, many_gates, by_gate) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_RS_ERR_CUDA;
-  }
-  return GEMM_RS_OK;
+  return launch_overlapped(norm_join_kernel, dim3((unsigned)((p.D + 31) / 32), (unsigned)(2 + crossing)), 256, 0, st, p,
+                           many_gates, by_gate);
 }

@@ -1,5 +1,5 @@
 // ops_common.cuh -- shared by the operators around the row-parallel layer:
-// device check, launch status, bf16 vectors and block-wide sums.
+// device check, launches and their status.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -62,44 +62,29 @@ class SmemAllowed {
   std::atomic<uint64_t> done_{0};
 };
 
+// Launch with programmatic dependent launch: the kernel's blocks may be placed
+// while the previous kernel on the stream finishes.  Every kernel launched this
+// way calls griddep_wait() before it touches global memory.
+template <typename... P, typename... A>
+int launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                      const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_RS_ERR_CUDA;
+  }
+  return GEMM_RS_OK;
+}
+
 inline bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  f[0] = bf16lo_to_f32(v.x); f[1] = bf16hi_to_f32(v.x);
-  f[2] = bf16lo_to_f32(v.y); f[3] = bf16hi_to_f32(v.y);
-  f[4] = bf16lo_to_f32(v.z); f[5] = bf16hi_to_f32(v.z);
-  f[6] = bf16lo_to_f32(v.w); f[7] = bf16hi_to_f32(v.w);
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  uint4 v;
-  v.x = pack_bf16x2(f[0], f[1]);
-  v.y = pack_bf16x2(f[2], f[3]);
-  v.z = pack_bf16x2(f[4], f[5]);
-  v.w = pack_bf16x2(f[6], f[7]);
-  return v;
-}
-
-// Sum of each of the N values over the block, in every thread (the same bits
-// in each: the butterfly adds the same pairs on both sides).  `part` holds
-// 32 * N floats; a block alternates between two of them, so that one barrier
-// a sum is enough.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float* part) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x + 31) >> 5;
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) part[i * 32 + warp] = v[i];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lane < warps ? part[i * 32 + lane] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-}
 
 }  // namespace grs

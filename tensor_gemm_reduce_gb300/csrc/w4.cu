@@ -432,22 +432,9 @@ int launch(const W4Params& p, const Split& sp, cudaStream_t st) {
   const auto kernel = p.zeros ? w4_kernel<kTiles, kGroup, true> : w4_kernel<kTiles, kGroup, false>;
   static SmemAllowed allowed[2];
   if (!allowed[p.zeros != nullptr].set(kernel, kMaxSmem)) return GEMM_RS_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kRanks, (unsigned)sp.clusters);
-  cfg.blockDim = dim3(32 * sp.wn * sp.wk);
-  cfg.dynamicSmemBytes = (size_t)sp.smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_RS_ERR_CUDA;
-  }
-  return GEMM_RS_OK;
+  return launch_overlapped(kernel, dim3(kRanks, (unsigned)sp.clusters), 32 * sp.wn * sp.wk, (size_t)sp.smem, st, p);
 }
+
 template <int kTiles>
 int launch(const W4Params& p, const Split& sp, cudaStream_t st) {
   if (p.group == 32) return launch<kTiles, 32>(p, sp, st);
