@@ -17,6 +17,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPerThread = 8;  // elements: 16 bytes of bf16, 8 bytes of codes
 constexpr int kUnroll = 4;     // units of 8 elements in flight for a thread
+constexpr int kBlocksPerSm = 64;
 
 // n / d for n < 2^31 as a multiplication (Granlund and Montgomery's method: with
 // 2^(l-1) < d <= 2^l and mul = ceil(2^(31+l) / d) the error n (mul d - 2^(31+l)) is
@@ -110,8 +111,10 @@ __global__ void __launch_bounds__(kThreads) act8_save_kernel(const Act8Params p)
 __global__ void __launch_bounds__(kThreads) act8_restore_kernel(const Act8Params p) {
   const long long units = p.rows * (p.pitch / kPerThread);
   const long long stride = (long long)gridDim.x * kThreads;
-  griddep_launch_dependents();
   griddep_wait();
+  // only now: the backward kernel counts on every earlier kernel being complete
+  // when it starts, and waits for this one where it needs it
+  griddep_launch_dependents();
   for (long long u0 = (long long)blockIdx.x * kThreads + threadIdx.x; u0 < units; u0 += kUnroll * stride) {
     Place at[kUnroll];
     uint2 q[kUnroll];
@@ -140,7 +143,8 @@ int check_shape(int64_t M, int64_t K) {
   return GEMM_RS_OK;
 }
 
-int run(bool save, int64_t M, int64_t K, void* A, void* codes, void* scales, void* stream) {
+// blocks_per_sm bounds the grid.
+int run(bool save, int64_t M, int64_t K, void* A, void* codes, void* scales, void* stream, int blocks_per_sm) {
   int rc = check_shape(M, K);
   if (rc) return rc;
   if (M == 0 || K == 0) return GEMM_RS_OK;
@@ -163,7 +167,7 @@ int run(bool save, int64_t M, int64_t K, void* A, void* codes, void* scales, voi
   p.codes = static_cast<uint2*>(codes);
   p.scales = static_cast<uint8_t*>(scales);
   const long long blocks = (p.rows * p.pitch / kPerThread + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-  const int grid = (int)(blocks < 64ll * sms ? blocks : 64ll * sms);
+  const int grid = (int)(blocks < (long long)blocks_per_sm * sms ? blocks : (long long)blocks_per_sm * sms);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return launch_overlapped(save ? act8_save_kernel : act8_restore_kernel, dim3((unsigned)grid), kThreads, 0, st, p);
 }
@@ -183,10 +187,14 @@ extern "C" int gemm_rs_act8_layout(int64_t M, int64_t K, int64_t* pitch, size_t*
 
 extern "C" int gemm_rs_act8_save(int64_t M, int64_t K, const void* A, void* codes, void* scales,
                                  void* stream) {
-  return run(true, M, K, const_cast<void*>(A), codes, scales, stream);
+  return run(true, M, K, const_cast<void*>(A), codes, scales, stream, kBlocksPerSm);
 }
 
 extern "C" int gemm_rs_act8_restore(int64_t M, int64_t K, const void* codes, const void* scales,
                                     void* A, void* stream) {
-  return run(false, M, K, A, const_cast<void*>(codes), const_cast<void*>(scales), stream);
+  return run(false, M, K, A, const_cast<void*>(codes), const_cast<void*>(scales), stream, kBlocksPerSm);
+}
+
+int grs::act8_restore_beside(int64_t M, int64_t K, const void* codes, const void* scales, void* A, void* stream) {
+  return run(false, M, K, A, const_cast<void*>(codes), const_cast<void*>(scales), stream, 2);
 }

@@ -40,6 +40,10 @@ constexpr int kNumBars = 2 * kStages + 5;  // full, empty, acc_full[2], acc_empt
 constexpr int kSmemMisc = kSmemBar + kNumBars * 8;
 constexpr int kSmemAlloc = kSmemMisc + 16 + 1024;  // slack to align the base to 1024 bytes
 static_assert(kSmemAlloc <= 232448, "shared memory per CTA");
+// Elements of a checkpoint up to which it is restored beside the dA tiles (M x N x K:
+// 392 x 776 x 1600 11.7 -> 11.1 us, 128 x 8192 x 8192 59.3 -> 57.7; above, 480 x 256 x
+// 12928 16.0 -> 17.0, 1000 x 1032 x 6400 35.8 -> 37.1, the largest no difference).
+constexpr int64_t kRestoreBeside = 2 << 20;
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
 
 // One of the two products: 8 ranks of mt x nt tiles, kb steps of kBK each.
@@ -105,6 +109,7 @@ struct BwdParams {
   Schedule s;
   int M, N, Kr;
   uint32_t* error;  // [0] non-zero once a wait gave up
+  int restored_before;  // the launch before this one restores A and lets this one start early
   unsigned long long timeout_ns;
 };
 
@@ -168,7 +173,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  griddep_wait();
+  // restored_before: the kernel before this one is the checkpoint's restoration,
+  // which lets this grid start when everything before it is complete, so the dA
+  // tiles need not wait; the A loader waits for it before the first dW tile.
+  if (!p.restored_before) griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const uint32_t tmem_base = *tmem_slot;
   TileWalk walk(pair);
@@ -181,8 +189,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
       const uint32_t base = sbase + (is_a ? 0 : kSmemB);
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_par = 0;
-      bool ok = true;
+      bool ok = true, waited = !p.restored_before;
       while (ok && walk.next(p.s, &t)) {
+        if (is_a && t.is_dw && !waited) {
+          griddep_wait();
+          fence_proxy_async_global();  // the restored values, before TMA reads them
+          waited = true;
+        }
         const int kb_count = t.is_dw ? p.s.dw.kb : p.s.da.kb;
         // first row (A) or column (B) of this CTA's half of the operand
         const int x0 = (is_a ? t.mt : t.nt) * kTile + cta * 128;
@@ -502,7 +515,11 @@ extern "C" int gemm_rs_bwd_run(gemm_rs_bwd_t h, const void* dY, const void* W, c
   if (dw) {
     ok = ok && make_map(&p.a_mn, workspace, h->Kr, h->M, kWorld, 64, kBK) &&
          make_map(&p.dy_mn, dY, h->N, h->M, 1, 64, kBK) && make_map(&p.out_dw, dW, h->N, h->Kr, kWorld, 64, 32);
-    const int rc = gemm_rs_act8_restore(h->M, h->K, codes, scales, workspace, stream);
+    // A small checkpoint is restored beside the first dA tiles; a large one is
+    // faster with the whole GPU to itself.
+    p.restored_before = da && h->M * h->K <= kRestoreBeside;
+    const int rc = p.restored_before ? act8_restore_beside(h->M, h->K, codes, scales, workspace, stream)
+                                     : gemm_rs_act8_restore(h->M, h->K, codes, scales, workspace, stream);
     if (rc) return rc;
   }
   if (!ok) return GEMM_RS_ERR_CUDA;
