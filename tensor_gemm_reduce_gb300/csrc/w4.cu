@@ -36,6 +36,7 @@ constexpr int kBlockN = 32;         // columns that lie together in the packed w
 constexpr int kCell = 64;           // inner elements of a lane's 16-byte load
 constexpr int kUnit = 128;          // inner elements of a step: two cells of each half
 constexpr int kMaxTokens = 32;
+constexpr int kPrefetchUnits = 8;   // units of a warp asked for before the previous grid ends
 constexpr int kMaxSmem = 227 * 1024;
 // Warps that an SM holds at 128 registers a thread, and that run at once on the
 // 148 SMs that clusters of 8 CTAs reach.
@@ -78,6 +79,7 @@ struct W4Params {
   int blocks, units, groups;   // units and groups of a rank
   int wn, wk;                  // warps of a CTA: wn of columns x wk parts of the units
   int part_units;              // units of a part
+  int prefetch_units;          // of each warp, before the previous grid ends
   int chunks, chunk_units, pitch;  // a part's inputs arrive in chunks: units, row pitch in bytes
   const uint16_t* x;           // [8][M][Kr]
   const uint4* weights;
@@ -104,6 +106,10 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
+// Multiples of 16 bytes.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -128,9 +134,9 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(256, 2)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t inputs = (uint32_t)(part * 2 * p.M * p.pitch);  // this part's chunks
   // The next launch's blocks may take the places that this one's leave; they
-  // touch no memory before this grid is complete.
+  // read and write no memory before this grid is complete, but bring their first
+  // weights to L2 (a hint, which sees whatever is written until they are read).
   griddep_launch_dependents();
-  griddep_wait();
   // every CTA of the cluster is running before any writes into another's memory
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
@@ -185,6 +191,12 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(256, 2)
       if (kZeros) v.z[b] = __ldcs(zp + d * kPerUnit * 16 + 8 * b);
     }
   };
+  const int early = u1 - u0 < p.prefetch_units ? u1 - u0 : p.prefetch_units;
+  if (lane == 0 && half0 == 0 && early > 0) {
+    prefetch_l2(wp, (uint32_t)early * 2048);
+    prefetch_l2(p.scales + (at * p.groups + (long long)u0 * kPerUnit) * 16, (uint32_t)(early * kPerUnit * 64));
+  }
+  griddep_wait();
   Unit ring[kDepth];
 #pragma unroll
   for (int d = 0; d < kDepth; ++d) fetch(ring[d], d, u0 + d < u1);
@@ -405,6 +417,7 @@ int check(int64_t M, int64_t N, int64_t K, int group) {
 // nothing at 8192 columns: 112 columns on 148 SMs as long as 128 on 128.)
 struct Split {
   int wn, wk, clusters, part_units, chunk_units, pitch, smem;
+  bool at_once;  // every cluster runs from the start
 };
 // Clusters of 8 CTAs that run at once with n CTAs an SM.
 constexpr int kMaxPerSm = 4;
@@ -425,10 +438,10 @@ Split split_of(int64_t M, int64_t N, int units, int tiles, const Slots& slots) {
   if (s.wk < 1) s.wk = 1;
   s.part_units = (units + s.wk - 1) / s.wk;
   s.wk = (units + s.part_units - 1) / s.part_units;
-  // the inputs' chunks: up to 8 units, an even number (a warp copies two at a time),
+  // the inputs' chunks: up to 32 units, an even number (a warp copies two at a time),
   // within the shared memory of as many CTAs as an SM's registers hold
   const int room = kMaxSmem / (kSmWarps / (s.wn * s.wk)) - 2 * 1024;
-  for (int most = s.part_units < 8 ? s.part_units : 8;; most = most > 2 ? (most - 1) / 2 * 2 : 1) {
+  for (int most = s.part_units < 32 ? s.part_units : 32;; most = most > 2 ? (most - 1) / 2 * 2 : 1) {
     s.chunk_units = most;
     s.pitch = s.chunk_units * kUnit * 2 + 64;  // two rows that 8 lanes read lie in different banks
     s.smem = (int)(s.wk * M * (2 * s.pitch + half_cols * s.wn * 4));  // and the shares
@@ -438,9 +451,10 @@ Split split_of(int64_t M, int64_t N, int units, int tiles, const Slots& slots) {
   // without work: no more CTAs an SM than the clusters need to run at once (6144
   // columns, K = 16384: 3 on 128 SMs instead of 4 on 96, one token 15.8 -> 13.8 us,
   // 16 tokens 24.3 -> 20.5).
-  for (int n = 1; n < kMaxPerSm; ++n)
+  for (int n = 1; n <= kMaxPerSm; ++n)
     if (slots.at[n] >= s.clusters) {
-      if (s.smem < smem_for(n)) s.smem = smem_for(n);
+      if (n < kMaxPerSm && s.smem < smem_for(n)) s.smem = smem_for(n);
+      s.at_once = true;
       break;
     }
   return s;
@@ -578,6 +592,8 @@ extern "C" int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int ha
   p.chunk_units = sp.chunk_units;
   p.chunks = (sp.part_units + sp.chunk_units - 1) / sp.chunk_units;
   p.pitch = sp.pitch;
+  // (in a second wave the request would come when the weights are read anyway)
+  p.prefetch_units = sp.at_once ? kPrefetchUnits : 0;
   p.x = static_cast<const uint16_t*>(x);
   p.weights = reinterpret_cast<const uint4*>(base);
   p.scales = reinterpret_cast<const uint32_t*>(base + l.scale_off);
