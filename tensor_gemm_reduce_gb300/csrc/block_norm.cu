@@ -546,16 +546,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   }
 }
 
-// Joins the blocks' sums, 32 columns a block: warp w adds rows w, w + 8, ...
-// and the eight sums are added in order.  blockIdx.y: 0 dw_pre, 1 dw_post (and
-// dgate when there is one gate row), from 2 on the gate rows that cross a chunk
-// border: gate row blockIdx.y - 2 if there are fewer gate rows than chunks,
-// else the one that crosses the border after chunk blockIdx.y - 2 as its first.
-__global__ void __launch_bounds__(256) norm_join_kernel(const NormParams p, int many_gates, int by_gate) {
-  __shared__ float part[8][32];
+// Joins the blocks' sums, 128 columns a block: warp w adds rows w, w + 16, ...,
+// four columns a lane and all of its rows' loads in flight at once, and the
+// sixteen sums are added in order.  blockIdx.y: 0 dw_pre, 1 dw_post (and dgate
+// when there is one gate row), from 2 on the gate rows that cross a chunk border:
+// gate row blockIdx.y - 2 if there are fewer gate rows than chunks, else the one
+// that crosses the border after chunk blockIdx.y - 2 as its first.
+constexpr int kJoinWarps = 16, kJoinCols = 128;
+__global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const NormParams p, int many_gates, int by_gate) {
+  __shared__ float part[kJoinWarps][kJoinCols];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
-  const bool in = col < p.D;
+  const int col = blockIdx.x * kJoinCols + 4 * lane;
   const int job = blockIdx.y;
   griddep_launch_dependents();
   griddep_wait();
@@ -577,30 +578,47 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const NormParams p, int 
     step = 2ll * p.D;
     odd = first > b * p.chunk_rows;  // chunk b's slot; the later chunks' are even
   }
-  float s = 0.f;
-  if (in)
-    for (int k = warp; k < n; k += 8) s += src[k * step + (odd && k == 0 ? p.D : 0) + col];
-  part[warp][lane] = s;
-  __syncthreads();
-  if (warp != 0 || !in) return;
-  s = part[0][lane];
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kBatch = (kBlocks + kJoinWarps - 1) / kJoinWarps;
+  if (col < p.D)
+    for (int k0 = warp; k0 < n; k0 += kJoinWarps * kBatch) {
+      float4 v[kBatch];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) s += part[w][lane];
+      for (int i = 0; i < kBatch; ++i) {
+        const int k = k0 + kJoinWarps * i;
+        if (k < n) v[i] = __ldcg(reinterpret_cast<const float4*>(src + k * step + (odd && k == 0 ? p.D : 0) + col));
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (k0 + kJoinWarps * i < n) {
+          s.x += v[i].x;
+          s.y += v[i].y;
+          s.z += v[i].z;
+          s.w += v[i].w;
+        }
+    }
+  *reinterpret_cast<float4*>(&part[warp][4 * lane]) = s;
+  __syncthreads();
+  const int c = blockIdx.x * kJoinCols + (int)threadIdx.x;
+  if (threadIdx.x >= kJoinCols || c >= p.D) return;
+  float f = part[0][threadIdx.x];
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) f += part[w][threadIdx.x];
   auto bf = [](const uint4* base, long long k) {
     return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[k] << 16);
   };
-  auto put = [](uint4* base, long long k, float f) {
-    reinterpret_cast<uint16_t*>(base)[k] = (uint16_t)(pack_bf16x2(f, 0.f) & 0xffffu);
+  auto put = [](uint4* base, long long k, float v) {
+    reinterpret_cast<uint16_t*>(base)[k] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
   };
   if (job == 0) {
-    put(p.dw_pre, col, s);
+    put(p.dw_pre, c, f);
   } else if (job == 1 && many_gates) {
-    put(p.dw_post, col, p.scale * s);
+    put(p.dw_post, c, p.scale * f);
   } else if (job == 1) {
-    put(p.dw_post, col, p.gate ? p.scale * bf(p.gate, col) * s : p.scale * s);
-    if (p.gate) put(p.dgate, col, p.scale * bf(p.w_post, col) * s);
+    put(p.dw_post, c, p.gate ? p.scale * bf(p.gate, c) * f : p.scale * f);
+    if (p.gate) put(p.dgate, c, p.scale * bf(p.w_post, c) * f);
   } else {
-    put(p.dgate, gi * p.D + col, p.scale * bf(p.w_post, col) * s);
+    put(p.dgate, gi * p.D + c, p.scale * bf(p.w_post, c) * f);
   }
 }
 
@@ -782,6 +800,7 @@ extern "C" int gemm_rs_norm_backward(const gemm_rs_norm_desc* d, const void* dr,
   if (rc) return rc;
   const int many_gates = mode != kSingle, by_gate = d->gate_rows < sp.chunks;
   const long long crossing = mode != kSequence ? 0 : by_gate ? d->gate_rows : sp.chunks - 1;
-  return launch_overlapped(norm_join_kernel, dim3((unsigned)((p.D + 31) / 32), (unsigned)(2 + crossing)), 256, 0, st, p,
+  return launch_overlapped(norm_join_kernel, dim3((unsigned)((p.D + kJoinCols - 1) / kJoinCols), (unsigned)(2 + crossing)),
+                           32 * kJoinWarps, 0, st, p,
                            many_gates, by_gate);
 }
