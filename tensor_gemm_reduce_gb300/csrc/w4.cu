@@ -329,31 +329,46 @@ struct PackParams {
   uint16_t* out_zeros;
 };
 
-// One 32-bit word (8 codes) a thread, then the groups' scales and zero points.
+// A block takes 64 inner elements x 128 columns at a time through shared memory:
+// rows come in whole 128-byte lines, each warp packs one cell of 16 columns.
+// Then the groups' scales and zero points.
 __global__ void __launch_bounds__(256) w4_pack_kernel(const PackParams p) {
+  constexpr int kCols = 128, kPitch = kCols + 4;  // 4 bytes beyond, so that rows 8 apart lie in other banks
+  __shared__ uint8_t tile[kCell * kPitch];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cells = 2 * p.units;
+  const long long items = (long long)((p.N + kCols - 1) / kCols) * kRanks * cells;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const int c = (int)(item % cells), r = (int)(item / cells % kRanks);
+    const int n0 = (int)(item / cells / kRanks) * kCols;
+    __syncthreads();  // the previous item's tile has been read
+    for (int i = threadIdx.x; i < kCell * kCols / 8; i += blockDim.x) {
+      const int row = i / (kCols / 8), seg = i % (kCols / 8);
+      const int k = c * kCell + row, n = n0 + 8 * seg;  // N is a multiple of 8
+      uint2 v = make_uint2(0, 0);
+      if (k < p.Kr && n < p.N) v = __ldcs(reinterpret_cast<const uint2*>(p.codes + ((long long)r * p.Kr + k) * p.N + n));
+      uint32_t* to = reinterpret_cast<uint32_t*>(tile + row * kPitch + 8 * seg);
+      to[0] = v.x & 0x0F0F0F0Fu;
+      to[1] = v.y & 0x0F0F0F0Fu;
+    }
+    __syncthreads();
+    const int block = n0 / kBlockN + warp / 2, half = warp & 1;
+    if (block >= p.blocks) continue;
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int step = 0; step < 4; ++step)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int reg = e >> 1;  // MMA register: column g or g + 8, inner pair 0 or 1
+        const int k = 32 * (step >> 1) + 8 * (lane & 3) + 4 * (step & 1) + 2 * (reg >> 1) + (e & 1);
+        const int n = warp * 16 + (lane >> 2) + 8 * (reg & 1);
+        w[step] |= (uint32_t)tile[k * kPitch + n] << (4 * reg + 16 * (e & 1));
+      }
+    const long long at = ((((long long)block * kRanks + r) * p.units + c / 2) * 2 + half) * 2 + (c & 1);
+    reinterpret_cast<uint4*>(p.weights)[at * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
   const long long stride = (long long)gridDim.x * blockDim.x;
   const long long first = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long words = (long long)p.blocks * kRanks * p.units * 512;
-  for (long long i = first; i < words; i += stride) {
-    const int step = (int)(i & 3), lane = (int)(i >> 2) & 31;
-    const long long cell = i >> 7;
-    const int half = (int)(cell >> 1) & 1;
-    const long long unit = cell >> 2;
-    const int c = (int)(unit % p.units) * 2 + (int)(cell & 1);
-    const int r = (int)(unit / p.units % kRanks);
-    const int block = (int)(unit / p.units / kRanks);
-    const int k0 = c * kCell + 32 * (step >> 1) + 8 * (lane & 3) + 4 * (step & 1);
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i4 = e >> 1;  // MMA register: column g or g + 8, inner pair 0 or 1
-      const int n = block * kBlockN + half * 16 + (lane >> 2) + 8 * (i4 & 1);
-      const int k = k0 + 2 * (i4 >> 1) + (e & 1);
-      if (n < p.N && k < p.Kr)
-        w |= (uint32_t)(p.codes[((long long)r * p.Kr + k) * p.N + n] & 15u) << (4 * i4 + 16 * (e & 1));
-    }
-    p.weights[i] = w;
-  }
   const long long metas = (long long)p.blocks * kRanks * p.groups * 16;
   for (long long i = first; i < metas; i += stride) {
     const int g = (int)(i & 7), half = (int)(i >> 3) & 1;
