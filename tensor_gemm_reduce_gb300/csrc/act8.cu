@@ -143,8 +143,9 @@ int check_shape(int64_t M, int64_t K) {
   return GEMM_RS_OK;
 }
 
-// blocks_per_sm bounds the grid.
-int run(bool save, int64_t M, int64_t K, void* A, void* codes, void* scales, void* stream, int blocks_per_sm) {
+// blocks_per_sm bounds the grid; padded: A's rows are as far apart as the codes'.
+int run(bool save, int64_t M, int64_t K, void* A, void* codes, void* scales, void* stream, int blocks_per_sm,
+        bool padded = false) {
   int rc = check_shape(M, K);
   if (rc) return rc;
   if (M == 0 || K == 0) return GEMM_RS_OK;
@@ -157,6 +158,7 @@ int run(bool save, int64_t M, int64_t K, void* A, void* codes, void* scales, voi
   p.rows = kWorld8 * M;
   p.cols = K / kWorld8;
   p.pitch = act8_pitch(K / kWorld8);
+  if (padded) p.cols = p.pitch;
   if (p.pitch == p.cols) {  // rows follow one another: one long row, no division by its length
     p.cols *= p.rows;
     p.pitch = p.cols;
@@ -195,6 +197,7 @@ extern "C" int gemm_rs_act8_restore(int64_t M, int64_t K, const void* codes, con
   return run(false, M, K, A, const_cast<void*>(codes), const_cast<void*>(scales), stream, kBlocksPerSm);
 }
 
-int grs::act8_restore_beside(int64_t M, int64_t K, const void* codes, const void* scales, void* A, void* stream) {
-  return run(false, M, K, A, const_cast<void*>(codes), const_cast<void*>(scales), stream, 2);
+int grs::act8_restore_padded(int64_t M, int64_t K, const void* codes, const void* scales, void* A, bool beside,
+                             void* stream) {
+  return run(false, M, K, A, const_cast<void*>(codes), const_cast<void*>(scales), stream, beside ? 2 : kBlocksPerSm, true);
 }

@@ -12,9 +12,11 @@ constexpr int kAct8Group = 32;  // elements of a row that share a scale
 // Codes of a row of `cols` elements, in whole 128-byte lines.
 inline int64_t act8_pitch(int64_t cols) { return (cols + 127) / 128 * 128; }
 
-// gemm_rs_act8_restore with two blocks an SM, which leave room for a block of the
-// backward kernel beside them; that kernel may start before this one has ended.
-int act8_restore_beside(int64_t M, int64_t K, const void* codes, const void* scales, void* A, void* stream);
+// gemm_rs_act8_restore into rows act8_pitch(K / 8) elements apart, zero beyond
+// the row's end.  `beside`: with two blocks an SM, which leave room for a block of
+// the backward kernel; that kernel may start before this one has ended.
+int act8_restore_padded(int64_t M, int64_t K, const void* codes, const void* scales, void* A, bool beside,
+                        void* stream);
 
 // Scale byte b stands for 2^(b - 127), whose bf16 pattern is b << 7; 255 gives
 // infinity, and its group's codes are zero, so their product is NaN.  Byte 0

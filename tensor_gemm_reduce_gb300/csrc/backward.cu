@@ -378,13 +378,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// bf16 [planes][rows][cols], 128-byte swizzle, zero fill out of bounds.
+// bf16 [planes][rows][cols], rows `pitch` elements apart (0: cols), 128-byte
+// swizzle, zero fill out of bounds.
 bool make_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t planes, uint32_t box_cols,
-              uint32_t box_rows) {
+              uint32_t box_rows, int64_t pitch = 0) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * (cuuint64_t)rows * 2};
+  const cuuint64_t row_bytes = (cuuint64_t)(pitch ? pitch : cols) * 2;
+  const cuuint64_t strides[2] = {row_bytes, row_bytes * (cuuint64_t)rows};
   const cuuint32_t box[3] = {box_cols, box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
@@ -469,7 +471,7 @@ extern "C" int gemm_rs_bwd_create(int64_t M, int64_t N, int64_t K, uint64_t time
   h->Kr = Kr;
   h->timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
   h->max_pairs = pairs < sms / 2 ? pairs : sms / 2;
-  h->a_bytes = ((size_t)kWorld * M * Kr * 2 + 255) / 256 * 256;
+  h->a_bytes = (size_t)kWorld * M * act8_pitch(Kr) * 2;  // whole 256-byte lines: TMA reads boxes of 128
   h->total = h->a_bytes + 256;
   if (workspace_bytes) *workspace_bytes = h->total;
   *plan = h;
@@ -513,13 +515,12 @@ extern "C" int gemm_rs_bwd_run(gemm_rs_bwd_t h, const void* dY, const void* W, c
     ok = ok && make_map(&p.dy_k, dY, h->N, h->M, 1, kBK, 128) && make_map(&p.w_k, W, h->N, h->Kr, kWorld, kBK, 128) &&
          make_map(&p.out_da, dA, h->Kr, h->M, kWorld, 64, 32);
   if (dw) {
-    ok = ok && make_map(&p.a_mn, workspace, h->Kr, h->M, kWorld, 64, kBK) &&
+    ok = ok && make_map(&p.a_mn, workspace, h->Kr, h->M, kWorld, 64, kBK, act8_pitch(h->Kr)) &&
          make_map(&p.dy_mn, dY, h->N, h->M, 1, 64, kBK) && make_map(&p.out_dw, dW, h->N, h->Kr, kWorld, 64, 32);
     // A small checkpoint is restored beside the first dA tiles; a large one is
     // faster with the whole GPU to itself.
     p.restored_before = da && h->M * h->K <= kRestoreBeside;
-    const int rc = p.restored_before ? act8_restore_beside(h->M, h->K, codes, scales, workspace, stream)
-                                     : gemm_rs_act8_restore(h->M, h->K, codes, scales, workspace, stream);
+    const int rc = act8_restore_padded(h->M, h->K, codes, scales, workspace, p.restored_before, stream);
     if (rc) return rc;
   }
   if (!ok) return GEMM_RS_ERR_CUDA;
