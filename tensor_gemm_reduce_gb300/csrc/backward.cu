@@ -406,6 +406,11 @@ Product product_of(int64_t rows, int64_t cols, int64_t depth) {
   return p;
 }
 
+// Estimated cycles of a tile: dA's steps, with the loads behind the tensor cores'
+// 512 cycles; dW's, of which a short one is as long as its 128 KB of output take.
+int da_tile_cycles(int kb) { return 600 * kb + 1000; }
+int dw_tile_cycles(int kb) { return (512 * kb > 2500 ? 512 * kb : 2500) + 500; }
+
 Schedule schedule_of(const Product& da, const Product& dw, int max_pairs) {
   Schedule s;
   s.da = da;
@@ -415,7 +420,7 @@ Schedule schedule_of(const Product& da, const Product& dw, int max_pairs) {
   s.extra = da.tiles() % s.pairs;
   s.early = 0;
   if (s.extra > 0 && dw.tiles() > 0) {
-    s.early = da.kb / dw.kb;
+    s.early = da_tile_cycles(da.kb) / dw_tile_cycles(dw.kb);
     const int spare = s.pairs - s.extra;
     // as many whole rounds of early tiles as there are tiles for
     if (s.early > dw.tiles() / spare) s.early = dw.tiles() / spare;
