@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) act8_save_kernel(const Act8Params p)
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
       at[k] = place_of(p, u0 + k * stride, units);
-      x[k] = at[k].in ? __ldcs(p.a + at[k].a / kPerThread) : make_uint4(0, 0, 0, 0);
+      x[k] = at[k].in ? load_v4_stream(p.a + at[k].a / kPerThread) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) act8_restore_kernel(const Act8Params
     for (int k = 0; k < kUnroll; ++k) {
       at[k] = place_of(p, u0 + k * stride, units);
       if (at[k].in) {
-        q[k] = __ldcs(p.codes + at[k].code / kPerThread);
+        q[k] = load_v2_stream(p.codes + at[k].code / kPerThread);
         s[k] = p.scales[at[k].code / kAct8Group];
       }
     }

@@ -236,18 +236,18 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
   uint4* w_pre = ring + (size_t)(p.stages * kArrays) * p.groups * p.nv + group * p.nv + t;
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (t + v * T < p.nv) w_pre[v * T] = __ldg(p.w_pre + t + v * T);
+    if (t + v * T < p.nv) w_pre[v * T] = load_v4(p.w_pre + t + v * T);
   F2 gw[V][4];  // scale w_post, times the gate unless it is in the ring
   auto branch_weights = [&](uint32_t gate_row) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (t + v * T < p.nv) {
-        unpack8(__ldg(p.w_post + t + v * T), gw[v]);
+        unpack8(load_v4(p.w_post + t + v * T), gw[v]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * both(p.scale);
         if (!kGateRing && p.gate) {
           F2 g[4];
-          unpack8(__ldg(p.gate + gate_row * p.nv + t + v * T), g);
+          unpack8(load_v4(p.gate + gate_row * p.nv + t + v * T), g);
 #pragma unroll
           for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * g[j];
         }
@@ -400,13 +400,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
 #pragma unroll
     for (int j = 0; j < 4; ++j) S[v][j] = Ppre[v][j] = both(0.f);
     if (i < p.nv) {
-      unpack8(__ldg(p.w_post + i), gw[v]);
-      wq[v] = __ldg(p.w_pre + i);
+      unpack8(load_v4(p.w_post + i), gw[v]);
+      wq[v] = load_v4(p.w_pre + i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * both(p.scale);
       if (kMode == kSingle && p.gate) {
         F2 g[4];
-        unpack8(__ldg(p.gate + i), g);
+        unpack8(load_v4(p.gate + i), g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * g[j];
       }
@@ -416,14 +416,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
 
   int stage = 0;
   // the rows' statistics, one row ahead
-  float pn_next = m0 < m1 ? __ldg(p.stats + m0) : 0.f, qn_next = m0 < m1 ? __ldg(p.stats + p.M + m0) : 0.f;
+  float pn_next = m0 < m1 ? load_f32(p.stats + m0) : 0.f, qn_next = m0 < m1 ? load_f32(p.stats + p.M + m0) : 0.f;
   uint32_t it = 0;
 #pragma unroll 1
   for (uint32_t m = m0; m < m1; m += step, ++it) {
     const float pn = pn_next, qn = qn_next;
     if (m + step < m1) {
-      pn_next = __ldg(p.stats + m + step);
-      qn_next = __ldg(p.stats + p.M + m + step);
+      pn_next = load_f32(p.stats + m + step);
+      qn_next = load_f32(p.stats + p.M + m + step);
     }
     cp_async_wait(p.stages);
     const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
@@ -582,19 +582,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const NormPa
   constexpr int kBatch = (kBlocks + kJoinWarps - 1) / kJoinWarps;
   if (col < p.D)
     for (int k0 = warp; k0 < n; k0 += kJoinWarps * kBatch) {
-      float4 v[kBatch];
+      uint4 v[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int k = k0 + kJoinWarps * i;
-        if (k < n) v[i] = __ldcg(reinterpret_cast<const float4*>(src + k * step + (odd && k == 0 ? p.D : 0) + col));
+        if (k < n) v[i] = load_v4_stream(src + k * step + (odd && k == 0 ? p.D : 0) + col);
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
         if (k0 + kJoinWarps * i < n) {
-          s.x += v[i].x;
-          s.y += v[i].y;
-          s.z += v[i].z;
-          s.w += v[i].w;
+          s.x += __uint_as_float(v[i].x);
+          s.y += __uint_as_float(v[i].y);
+          s.z += __uint_as_float(v[i].z);
+          s.w += __uint_as_float(v[i].w);
         }
     }
   *reinterpret_cast<float4*>(&part[warp][4 * lane]) = s;

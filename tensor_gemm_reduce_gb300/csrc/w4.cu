@@ -23,8 +23,6 @@
 // distributed shared memory and adds the eight (in rank order) that it is handed:
 // the layer's reduce-scatter, inside one cluster.  Inside a CTA the warps take
 // columns, and where there are few columns also parts of the inner dimension.
-#include <mutex>
-
 #include "ops_common.cuh"
 
 using namespace grs;
@@ -185,10 +183,10 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(256, 2)
     if (!in) return;
 #pragma unroll
     for (int b = 0; b < kHalves; ++b) {
-      v.w[b][0] = __ldcs(wp + d * 128 + b * 64);
-      v.w[b][1] = __ldcs(wp + d * 128 + b * 64 + 32);
-      v.s[b] = __ldcs(sp + d * kPerUnit * 16 + 8 * b);
-      if (kZeros) v.z[b] = __ldcs(zp + d * kPerUnit * 16 + 8 * b);
+      v.w[b][0] = load_v4_stream(wp + d * 128 + b * 64);
+      v.w[b][1] = load_v4_stream(wp + d * 128 + b * 64 + 32);
+      v.s[b] = load_u32_stream(sp + d * kPerUnit * 16 + 8 * b);
+      if (kZeros) v.z[b] = load_u16_stream(zp + d * kPerUnit * 16 + 8 * b);
     }
   };
   const int early = u1 - u0 < p.prefetch_units ? u1 - u0 : p.prefetch_units;
@@ -478,31 +476,27 @@ Split split_of(int64_t M, int64_t N, int units, int tiles, const Slots& slots) {
 // Looked up once for each device, with a kernel of one warp (registers and warps
 // do not bound it).
 bool slots_of(Slots* out) {
-  static std::mutex mutex;
-  static Slots known[64];
-  static bool have[64];
+  static std::atomic<int> known[64][kMaxPerSm + 1];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-  std::lock_guard<std::mutex> lock(mutex);
-  if (!have[dev]) {
-    const auto kernel = w4_kernel<1, 128, false>;
-    static SmemAllowed allowed;
-    if (!allowed.set(kernel, kMaxSmem)) return false;
-    for (int n = 1; n <= kMaxPerSm; ++n) {
+  const auto kernel = w4_kernel<1, 128, false>;
+  for (int n = 1; n <= kMaxPerSm; ++n) {
+    int clusters = known[dev][n].load(std::memory_order_relaxed);
+    if (clusters == 0) {
+      static SmemAllowed allowed;
+      if (!allowed.set(kernel, kMaxSmem)) return false;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(kRanks, 1024);
       cfg.blockDim = dim3(32);
       cfg.dynamicSmemBytes = (size_t)smem_for(n);
-      int clusters = 0;
       if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters < 1) {
         cudaGetLastError();
         return false;
       }
-      known[dev].at[n] = clusters;
+      known[dev][n].store(clusters, std::memory_order_relaxed);
     }
-    have[dev] = true;
+    out->at[n] = clusters;
   }
-  *out = known[dev];
   return true;
 }
 

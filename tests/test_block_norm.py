@@ -98,7 +98,7 @@ def assert_close(got, ref, mag, steps, name):
 # fewer and more rows than chunks, gate rows that divide, straddle and equal the chunks
 SHAPES = [(1, 8, 0), (1, 8, 1), (3, 64, 3), (2, 264, 2), (5, 1000, 1), (1, 8192, 1), (152, 512, 8), (153, 520, 3),
           (304, 768, 4), (610, 256, 5), (700, 128, 350), (1003, 136, 1003), (960, 72, 6), (17, 4104, 0),
-          (9, 8200, 3), (6, 12288, 2), (4, 12296, 1), (5, 16384, 5), (1520, 1032, 10), (2048, 520, 256), (1050, 264, 150)]
+          (9, 8200, 3), (6, 12288, 2), (4, 12296, 1), (5, 16384, 5), (6, 16384, 2), (1520, 1032, 10), (2048, 520, 256), (1050, 264, 150)]
 
 
 @pytest.mark.gpu
