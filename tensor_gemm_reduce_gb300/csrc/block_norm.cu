@@ -59,9 +59,9 @@ Shape shape_of(int nv, int arrays, long long rows, int blocks, int budget, int e
   return s;
 }
 
-// Where the gate comes from: one row (or none) is held in registers like the
-// weights; a row for some rows each (kSequence) or for each row (kElement)
-// goes through the ring with the row's other inputs.
+// Where the backward pass has the gate: one row (or none) is held in registers
+// like the weights; a row for some rows each (kSequence) or for each row
+// (kElement) goes through the ring with the row's other inputs.
 enum GateMode : int { kSingle = 0, kSequence = 1, kElement = 2 };
 
 struct NormParams {
@@ -76,10 +76,10 @@ struct NormParams {
   // backward
   const uint4 *dr, *dh;
   uint4 *dx, *dy, *dgate, *dw_post, *dw_pre;
-  // Rows of a group: chunk_rows consecutive ones (step = 1) where a gate row
-  // serves several of them, else rows `step` = the number of groups apart, so
-  // that all blocks work on one region of memory at a time (8192 x 8192: 101 ->
-  // 96 us forward, 133 -> 127 us backward).
+  // Rows of a group: `step` = the number of groups apart, so that all blocks
+  // work on one region of memory at a time (8192 x 8192: 101 -> 96 us forward,
+  // 133 -> 127 us backward); in the backward pass with a gate row for some rows
+  // each, chunk_rows consecutive ones (step = 1), whose sums stay in registers.
   uint32_t chunk_rows, step;
   int chunks, blocks;
   float *part_post, *part_pre, *part_gate;
@@ -198,34 +198,38 @@ constexpr int forward_blocks(int v) { return v <= 2 ? 2 : 1; }
 // The row stays in the ring until it is written and is unpacked twice: keeping
 // it in registers spilled some of them, and with most of the SM's memory given
 // to the ring every spill went to L2.
-// A gate row that serves several consecutive rows of a group stays in registers
-// with w_post; kGateRing: gate rows change too often for
-// that and arrive through the ring.
-template <int V, bool kGateRing>
+// The gate's row comes through the ring beside x and y, from L2 where it serves
+// several rows; without a gate w_post comes that way, and the registers hold
+// scale alone.  Measured against a gate row (or none) held in registers with
+// w_post, which is loaded again where the next gate row begins: 84.5 against
+// 93.5 us on 8192 x 8192 without a gate, 84.9 against 96.4 with 32 gate rows,
+// 25.4 against 27.7 on 2048 x 8192 with 4, 46.2 against 49.2 on 32768 x 1024;
+// behind only where L2 takes the writes and there is one gate row or none: 25.1
+// against 23.8 on 2048 x 8192, 16.0 against 15.1 on 1024 x 8192.
+template <int V>
 __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_kernel(const NormParams p) {
   extern __shared__ uint4 ring[];
   __shared__ float part[2][4][kMaxWarps];
-  constexpr int kArrays = kGateRing ? 3 : 2;
+  constexpr int kArrays = 3;
   const int group = (int)(threadIdx.x >> 5) / p.warps, T = 32 * p.warps;
   const int t = threadIdx.x - group * T;
   const uint32_t mine = smem_u32(ring) + 16u * (group * p.nv + t);
   const uint32_t plane = 16u * p.groups * p.nv;  // one array of a stage
-  const uint32_t c = blockIdx.x * p.groups + group, step = p.step;
-  const uint32_t m0 = step == 1 ? c * p.chunk_rows : c;
-  const uint32_t m1 = step == 1 && m0 + p.chunk_rows < p.M ? m0 + p.chunk_rows : p.M;
+  const uint32_t m0 = blockIdx.x * p.groups + group, m1 = p.M, step = p.step;
   griddep_launch_dependents();  // the next launch's blocks take the places that free up, and wait
   griddep_wait();
 
+  const uint4* factor = p.gate ? p.gate : p.w_post;
   auto fetch = [&](uint32_t row, int stage) {
     if (row < m1) {
       const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
-      const uint32_t at = row * p.nv + t, gat = kGateRing ? row / p.rows_per_gate * p.nv + t : 0;
+      const uint32_t at = row * p.nv + t, gat = (p.gate ? row / p.rows_per_gate * p.nv : 0) + t;
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (t + v * T < p.nv) {
           cp_async16(base + 16u * v * T, p.y + (at + v * T));
           cp_async16(base + plane + 16u * v * T, p.x + (at + v * T));
-          if (kGateRing) cp_async16(base + 2 * plane + 16u * v * T, p.gate + (gat + v * T));
+          cp_async16(base + 2 * plane + 16u * v * T, factor + (gat + v * T));
         }
     }
     cp_async_commit();
@@ -237,42 +241,32 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
 #pragma unroll
   for (int v = 0; v < V; ++v)
     if (t + v * T < p.nv) w_pre[v * T] = load_v4(p.w_pre + t + v * T);
-  F2 gw[V][4];  // scale w_post, times the gate unless it is in the ring
-  auto branch_weights = [&](uint32_t gate_row) {
+  F2 gw[V][4];  // the branch's factors that are not in the ring
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (t + v * T < p.nv) {
-        unpack8(load_v4(p.w_post + t + v * T), gw[v]);
+  for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * both(p.scale);
-        if (!kGateRing && p.gate) {
-          F2 g[4];
-          unpack8(load_v4(p.gate + gate_row * p.nv + t + v * T), g);
+    for (int j = 0; j < 4; ++j) gw[v][j] = both(p.scale);
+    if (p.gate && t + v * T < p.nv) {
+      F2 w[4];
+      unpack8(load_v4(p.w_post + t + v * T), w);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * g[j];
-        }
-      }
-  };
-  uint32_t gate_row = p.gate ? m0 / p.rows_per_gate : 0, gate_end = p.gate ? (gate_row + 1) * p.rows_per_gate : p.M;
-  if (m0 < p.M) branch_weights(gate_row);
+      for (int j = 0; j < 4; ++j) gw[v][j] = w[j] * gw[v][j];
+    }
+  }
 
   int stage = 0;
   uint32_t it = 0;
 #pragma unroll 1
   for (uint32_t m = m0; m < m1; m += step, ++it) {
-    if (!kGateRing && m == gate_end) {
-      branch_weights(++gate_row);
-      gate_end += p.rows_per_gate;
-    }
     cp_async_wait(p.stages);
     const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
     // y, x and the branch c of one vector, from the ring
     auto load = [&](int v, F2 (&y)[4], F2 (&x)[4], F2 (&c)[4]) {
       unpack8(ld_shared_v4(base + 16u * v * T), y);
       unpack8(ld_shared_v4(base + plane + 16u * v * T), x);
-      if (kGateRing) unpack8(ld_shared_v4(base + 2 * plane + 16u * v * T), c);
+      unpack8(ld_shared_v4(base + 2 * plane + 16u * v * T), c);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] = kGateRing ? c[j] * gw[v][j] * y[j] : gw[v][j] * y[j];
+      for (int j = 0; j < 4; ++j) c[j] = c[j] * gw[v][j] * y[j];
     };
     F2 yy = both(0.f), xx = yy, xc = yy, cc = yy;
 #pragma unroll
@@ -680,10 +674,9 @@ int launch(const NormParams& p, int grid, int threads, int smem, cudaStream_t st
 }
 
 template <int V>
-int launch_forward(const NormParams& p, bool gate_ring, int grid, int smem, cudaStream_t st) {
+int launch_forward(const NormParams& p, int grid, int smem, cudaStream_t st) {
   const int threads = 32 * p.warps * p.groups;
-  return gate_ring ? launch<norm_forward_kernel<V, true>>(p, grid, threads, smem, st)
-                    : launch<norm_forward_kernel<V, false>>(p, grid, threads, smem, st);
+  return launch<norm_forward_kernel<V>>(p, grid, threads, smem, st);
 }
 template <int V>
 int launch_backward(const NormParams& p, GateMode mode, int smem, cudaStream_t st) {
@@ -714,24 +707,19 @@ extern "C" int gemm_rs_norm_forward(const gemm_rs_norm_desc* d, const void* x, c
   NormParams p = params_of(d);
   p.x = in(x); p.y = in(y); p.gate = in(gate); p.w_post = in(w_post); p.w_pre = in(w_pre);
   p.r = outp(r); p.h = outp(h); p.stats = static_cast<float*>(stats);
-  // a gate row in registers pays from 8 rows on: loading it stalls its group
-  const bool gate_ring = d->gate_rows > 1 && p.rows_per_gate < 8;
-  const int arrays = gate_ring ? 3 : 2;
-  Shape s = shape_of(p.nv, arrays, d->M, 2 * sms, kMaxSmem / 2, 16);
+  Shape s = shape_of(p.nv, 3, d->M, 2 * sms, kMaxSmem / 2, 16);
   const int per_sm = forward_blocks(s.v);
-  if (per_sm == 1) s = shape_of(p.nv, arrays, d->M, sms, kMaxSmem, 16);
+  if (per_sm == 1) s = shape_of(p.nv, 3, d->M, sms, kMaxSmem, 16);
   set_shape(&p, s);
-  const long long lanes = (long long)per_sm * sms * s.groups;
-  p.chunk_rows = (uint32_t)((d->M + lanes - 1) / lanes);
-  const long long chunks = (d->M + p.chunk_rows - 1) / p.chunk_rows;
-  const int grid = (int)((chunks + s.groups - 1) / s.groups);
-  p.step = d->gate_rows > 1 && !gate_ring ? 1 : (uint32_t)(grid * s.groups);
+  const long long rows = ((long long)d->M + s.groups - 1) / s.groups;  // of a block's groups together
+  const int grid = (int)(rows < (long long)per_sm * sms ? rows : (long long)per_sm * sms);
+  p.step = (uint32_t)(grid * s.groups);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (s.v) {
-    case 1: return launch_forward<1>(p, gate_ring, grid, s.smem, st);
-    case 2: return launch_forward<2>(p, gate_ring, grid, s.smem, st);
-    case 3: return launch_forward<3>(p, gate_ring, grid, s.smem, st);
-    default: return launch_forward<4>(p, gate_ring, grid, s.smem, st);
+    case 1: return launch_forward<1>(p, grid, s.smem, st);
+    case 2: return launch_forward<2>(p, grid, s.smem, st);
+    case 3: return launch_forward<3>(p, grid, s.smem, st);
+    default: return launch_forward<4>(p, grid, s.smem, st);
   }
 }
 

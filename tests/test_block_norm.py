@@ -94,7 +94,7 @@ def assert_close(got, ref, mag, steps, name):
                            f"{np.nanmax(np.abs(got - ref) / bound):.2f} x the bound")
 
 
-# rows and columns at the edges (gate rows of 7 and 8 rows too, where the gate's way in changes): one row, one vector, a ragged last warp, two to four vectors a thread,
+# rows and columns at the edges: one row, one vector, a ragged last warp, two to four vectors a thread,
 # fewer and more rows than chunks, gate rows that divide, straddle and equal the chunks
 SHAPES = [(1, 8, 0), (1, 8, 1), (3, 64, 3), (2, 264, 2), (5, 1000, 1), (1, 8192, 1), (152, 512, 8), (153, 520, 3),
           (304, 768, 4), (610, 256, 5), (700, 128, 350), (1003, 136, 1003), (960, 72, 6), (17, 4104, 0),
