@@ -23,6 +23,11 @@
 // distributed shared memory and adds the eight (in rank order) that it is handed:
 // the layer's reduce-scatter, inside one cluster.  Inside a CTA the warps take
 // columns, and where there are few columns also parts of the inner dimension.
+//
+// Measured, us: one token, 8192 columns, K = 28672 (121 MB) 23.8, 5.1 TB/s, 0.75 of
+// a copy's rate; K = 8192 9.5, where the clusters' start and joins count as much as
+// the weights.  16 tokens, 6144 columns, K = 16384 19.1; 32 tokens 32: 12 to 16
+// warps an SM hide too little of the latency of unpacking, MMA and scaling.
 #include "ops_common.cuh"
 
 using namespace grs;
@@ -36,16 +41,19 @@ constexpr int kUnit = 128;          // inner elements of a step: two cells of ea
 constexpr int kMaxTokens = 32;
 constexpr int kPrefetchUnits = 8;   // units of a warp asked for before the previous grid ends
 constexpr int kMaxSmem = 227 * 1024;
-// Warps that an SM holds at 128 registers a thread, and that run at once on the
-// 148 SMs that clusters of 8 CTAs reach.
-constexpr int kSmWarps = 16;
-constexpr int kRunningWarps = kSmWarps * 148;
+constexpr int kSmWarps = 16;        // that an SM holds at 128 registers a thread
 
 // Halves of a block that a warp multiplies (one set of input fragments serves
 // both, but 3 and 4 token tiles leave no registers for a second one), and units
-// of weights in flight for each warp.
+// of weights in flight for each warp: what leaves the fewest spills, which go to L2
+// where shared memory takes most of L1 (32 tokens, 6144 columns, K = 16384: 37 us
+// with 4 units, 33 with 3).
 __host__ __device__ constexpr int halves_of(int tiles) { return tiles <= 2 ? 2 : 1; }
-__host__ __device__ constexpr int depth_of(int tiles) { return tiles == 1 ? 3 : tiles == 2 ? 2 : 4; }
+__host__ __device__ constexpr int depth_of(int tiles) { return tiles == 2 ? 2 : 3; }
+
+// Tokens of a column of the shares: eight (32 bytes, what one store of a warp
+// writes of a column) or a multiple, or 2 or 4.
+__host__ __device__ constexpr int share_pitch(int M) { return M <= 2 ? 2 : M <= 4 ? 4 : (M + 7) / 8 * 8; }
 
 // Packed buffer: weights [N/32][8][units][2 halves][2 cells][32 lanes] of 16
 // bytes, then scales [N/32][8][groups][2 halves][8] of two bf16 (columns g and
@@ -108,8 +116,8 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, float a, float b) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
 // kTiles tiles of 8 tokens, groups of kGroup inner elements.
@@ -117,7 +125,7 @@ template <int kTiles, int kGroup, bool kZeros>
 __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(256, 2)
     w4_kernel(const W4Params p) {
   // for each part two chunks of the inputs [token][chunk]; then the ranks' and
-  // parts' shares of this CTA's columns [rank][part][token][column], which the
+  // parts' shares of this CTA's columns [rank][part][column][token], which the
   // cluster's CTAs write
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kHalves = halves_of(kTiles), kDepth = depth_of(kTiles);
@@ -138,12 +146,16 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(256, 2)
   // every CTA of the cluster is running before any writes into another's memory
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
-  // inputs of units [u, u + chunk_units) into buffer `buf`; zero beyond the row's end
+  // inputs of units [u, u + chunk_units) into buffer `buf`; zero beyond the row's
+  // end.  A row takes a warp, or with more than 8 tokens half of one where a chunk
+  // is one unit (16 tokens, 512 columns, K = 28672: 16.5 -> 10.4 us).
   auto stage_inputs = [&](int u, int buf) {
+    const int row_log = kTiles > 1 && p.chunk_units == 1 ? 4 : 5, row_lanes = 1 << row_log;
+    const int first = kTiles > 1 ? (int)(threadIdx.x - 32 * part * p.wn) >> row_log : wn;
     const int vectors = (u1 - u < p.chunk_units ? u1 - u : p.chunk_units) * (kUnit / 8);
-    for (int m = wn; m < p.M; m += p.wn) {
+    for (int m = first; m < p.M; m += (32 * p.wn) >> row_log) {
       const uint16_t* src = p.x + ((long long)rank * p.M + m) * p.Kr;
-      for (int v = lane; v < vectors; v += 32) {
+      for (int v = lane & (row_lanes - 1); v < vectors; v += row_lanes) {
         const int k = u * kUnit + 8 * v;
         const bool in = k < p.Kr;
         asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(
@@ -289,30 +301,34 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(256, 2)
   // holds all 16 of a CTA, and an SM has 64: no more than 4 CTAs.)
   for (; synced < p.chunks; ++synced) __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  // hand each CTA this warp's sums for its columns
+  // Hand each CTA this warp's sums for its columns, two tokens a lane and whole 32
+  // bytes a column: with only the tokens there are (5 tokens, 12288 columns, K =
+  // 4096) 11.6 instead of 11.0 us; 4-byte stores for each token, 13.7 instead of
+  // 10.2 at 16 tokens, 512 columns, K = 28672.
   const uint32_t shares = (uint32_t)(p.wk * 2 * p.M * p.pitch);
+  const int tokens = share_pitch(p.M);
 #pragma unroll
   for (int b = 0; b < kHalves; ++b)
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
+    for (int i = 0; i < 2; ++i) {
+      const int col = (wn * kHalves + b) * 16 + g + 8 * i, owner = col / share;
+      const uint32_t to = mapa_shared(sbase + shares, owner) +
+                          4u * (uint32_t)(((rank * p.wk + part) * share + col - owner * share) * tokens + 2 * q);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int m = 8 * t + 2 * q + (i & 1);
-        const int col = (wn * kHalves + b) * 16 + g + 8 * (i >> 1), owner = col / share;
-        if (m < p.M)
-          st_cluster_f32(mapa_shared(sbase + shares, owner) +
-                             4u * (uint32_t)(((rank * p.wk + part) * p.M + m) * share + col - owner * share),
-                         64.f * acc[b][t][i]);
-      }
+      for (int t = 0; t < kTiles; ++t)
+        if (8 * t + 2 * q < tokens) st_cluster_v2(to + 32u * t, 64.f * acc[b][t][2 * i], 64.f * acc[b][t][2 * i + 1]);
+    }
   cluster_sync();  // the shares of all ranks are here
 
   const float* from = reinterpret_cast<const float*>(smem + shares);
-  for (int i = threadIdx.x; i < share * p.M; i += blockDim.x) {
-    const int m = i / share;
-    const int n = tile * cols + rank * share + (i - m * share);
-    if (n >= p.N) continue;
+  // eight tokens of a column in eight lanes, then the next column
+  const int low = tokens < 8 ? tokens : 8;
+  for (int i = threadIdx.x; i < share * tokens; i += blockDim.x) {
+    const int c = i / low, block = c / share, col = c - block * share, m = block * low + i - c * low;
+    const int n = tile * cols + rank * share + col;
+    if (m >= p.M || n >= p.N) continue;
     float s = 0.f;
-    for (int r = 0; r < kRanks * p.wk; ++r) s += from[r * share * p.M + i];  // in order
+    for (int r = 0; r < kRanks * p.wk; ++r) s += from[(r * share + col) * tokens + m];  // in order
     p.out[(long long)m * p.N + n] = (uint16_t)(pack_bf16x2(s, 0.f) & 0xFFFFu);
   }
 }
@@ -422,12 +438,16 @@ int check(int64_t M, int64_t N, int64_t K, int group) {
 }
 
 // How the columns and the inner dimension are cut: clusters of 128 columns, and
-// fewer columns where that leaves under 32 clusters (256 CTAs); then as many
-// parts of the inner dimension as fill the warps that can run at once.
-// One token, us: 1024 columns, K = 28672: 16 columns x 8 parts 6.8, 64 x 2 11.0,
-// 128 x 1 15; 4096 columns, K = 8192: 128 x 2 6.9, 128 x 1 8.5; at 8192 columns
-// 128 x 1 9.6, 64 x 2 12.1.  (Narrower clusters for an even load of the SMs gained
-// nothing at 8192 columns: 112 columns on 148 SMs as long as 128 on 128.)
+// fewer columns where that leaves under 32 clusters (256 CTAs), down to a warp's,
+// or two warps' from 17 tokens on (every CTA copies all its rank's inputs: 32
+// tokens, 512 columns, K = 28672: 16 columns x 8 parts 30.8 us, 32 x 4 15.7).  Then
+// parts of the inner dimension: CTAs of 8 warps where two of them fit each SM at
+// once, else of 4, which fit four times (2560 columns, K = 8192, one token: 64
+// columns x 3 parts in two waves 7.3, 64 x 2 at once 4.9).  A warp's columns and up
+// to 4 tokens take 4 parts (1024 columns, K = 8192, one token 3.4 against 3.8 with
+// 8; 512 columns, K = 28672, 3 tokens 5.7 against 5.9, 6 tokens 7.8 against 6.8).
+// (Narrower clusters for an even load of the SMs gained nothing at 8192 columns:
+// 112 columns on 148 SMs as long as 128 on 128.)
 struct Split {
   int wn, wk, clusters, part_units, chunk_units, pitch, smem;
   bool at_once;  // every cluster runs from the start
@@ -443,10 +463,10 @@ Split split_of(int64_t M, int64_t N, int units, int tiles, const Slots& slots) {
   Split s = {};
   const int half_cols = 16 * halves_of(tiles);
   s.wn = 128 / half_cols;
-  while (s.wn > 1 && N <= 31ll * half_cols * s.wn) s.wn /= 2;
+  while (s.wn > (tiles > 2 ? 2 : 1) && N <= 31ll * half_cols * s.wn) s.wn /= 2;
   s.clusters = (int)((N + half_cols * s.wn - 1) / (half_cols * s.wn));
-  s.wk = kRunningWarps / (s.clusters * kRanks * s.wn);
-  if (s.wk > 8 / s.wn) s.wk = 8 / s.wn;
+  const bool eight = s.clusters <= slots.at[kSmWarps / 8] && !(M <= 4 && s.wn == 1);
+  s.wk = (eight ? 8 : 4) / s.wn;
   if (s.wk > units) s.wk = units;
   if (s.wk < 1) s.wk = 1;
   s.part_units = (units + s.wk - 1) / s.wk;
@@ -457,7 +477,7 @@ Split split_of(int64_t M, int64_t N, int units, int tiles, const Slots& slots) {
   for (int most = s.part_units < 32 ? s.part_units : 32;; most = most > 2 ? (most - 1) / 2 * 2 : 1) {
     s.chunk_units = most;
     s.pitch = s.chunk_units * kUnit * 2 + 64;  // two rows that 8 lanes read lie in different banks
-    s.smem = (int)(s.wk * M * (2 * s.pitch + half_cols * s.wn * 4));  // and the shares
+    s.smem = (int)(s.wk * (2 * M * s.pitch + share_pitch((int)M) * half_cols * s.wn * 4));  // and the shares
     if (most == 1 || s.smem <= room) break;
   }
   // The hardware packs clusters as densely as they fit and leaves the last SMs
