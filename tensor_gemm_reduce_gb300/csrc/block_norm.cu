@@ -18,6 +18,21 @@ constexpr int kBackwardSmem = 200 * 1024;
 // order of the sums do not depend on the device.
 constexpr int kBlocks = 152;
 
+// Where the backward pass has the gate: one row (or none) is held in registers
+// like the weights; a row for some rows each (kSequence) or for each row
+// (kElement) goes through the ring with the row's other inputs.
+enum GateMode : int { kSingle = 0, kSequence = 1, kElement = 2 };
+
+// In the backward pass three and four vectors a thread leave too few registers for
+// the weights, and spilled ones go to L2 where the ring takes most of L1: w_pre lies
+// in shared memory (w_post too, where shared memory holds both), and w_post stays
+// packed where the gate is not multiplied into it.  us, M x D: 4096 x 12288 with one
+// gate row 137.7 -> 101.8, with 4 170 -> 143, with 4096 164 -> 146; 2048 x 9912 75 ->
+// 57; 8192 x 4160 with 8 gate rows 133 -> 110.
+__host__ __device__ constexpr bool pre_in_shared(int v, int mode) { return v == 3 || (v == 4 && mode != kSequence); }
+__host__ __device__ constexpr bool post_in_shared(int v, int mode) { return v == 3 && mode == kSequence; }
+__host__ __device__ constexpr bool post_packed(int v, int mode) { return v >= 3 && mode != kSingle; }
+
 // A row belongs to a group of `warps` warps, thread t of the group holding its
 // 16-byte vectors t, t + 32 warps, ... (`v` of them at most); a block has
 // `groups` such groups, each with rows of its own.  Every thread copies the
@@ -27,7 +42,8 @@ constexpr int kBlocks = 152;
 struct Shape {
   int v, warps, groups, stages, smem;
 };
-Shape shape_of(int nv, int arrays, long long rows, int blocks, int budget, int extra_per_vector) {
+// backward: the pass's GateMode, or -1 for the forward pass.
+Shape shape_of(int nv, int arrays, long long rows, int blocks, int budget, int extra_per_vector, int backward = -1) {
   Shape s = {0, 0, 0, 0, 0};
   // Two vectors a thread unless that leaves more than a quarter of the warps out.
   int best = 0;
@@ -49,7 +65,12 @@ Shape shape_of(int nv, int arrays, long long rows, int blocks, int budget, int e
   const long long need = (rows + blocks - 1) / blocks;
   if (s.groups > need) s.groups = need < 1 ? 1 : (int)need;
   const int row = s.groups * nv * 16;
-  const int extra = s.groups * nv * extra_per_vector;
+  int extra = s.groups * nv * extra_per_vector;
+  if (backward >= 0 && pre_in_shared(s.v, backward)) {
+    const int weights = post_in_shared(s.v, backward) ? 2 * row : row;
+    extra += weights;
+    if (s.v == 3) budget = budget + weights < kMaxSmem ? budget + weights : kMaxSmem;
+  }
   s.stages = (budget - extra) / (arrays * row);
   // Two are enough: a third row in flight gained nothing on 8192 rows of 8192
   // and queued in front of the first row on 1003 (16.5 against 15.2 us).
@@ -58,11 +79,6 @@ Shape shape_of(int nv, int arrays, long long rows, int blocks, int budget, int e
   s.smem = s.stages * arrays * row + extra;
   return s;
 }
-
-// Where the backward pass has the gate: one row (or none) is held in registers
-// like the weights; a row for some rows each (kSequence) or for each row
-// (kElement) goes through the ring with the row's other inputs.
-enum GateMode : int { kSingle = 0, kSequence = 1, kElement = 2 };
 
 struct NormParams {
   uint32_t M;               // M * nv stays below 2^31: vector indexes are 32-bit
@@ -385,8 +401,18 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   };
   for (int s = 0; s < p.stages; ++s) fetch(m0 + s * step, s);
 
-  F2 gw[V][4];  // scale w_post, times the gate when there is one row of it
-  uint4 wq[V];
+  constexpr bool kPreShared = pre_in_shared(V, kMode), kPacked = post_packed(V, kMode);
+  F2 gw[kPacked ? 1 : V][4];  // scale w_post, times the gate when there is one row of it
+  constexpr bool kPostShared = post_in_shared(V, kMode);
+  uint4 wp[kPacked && !kPostShared ? V : 1], wq[kPreShared ? 1 : V];
+  // this thread's vectors of w_pre, after the ring and the columns of dw_post
+  const uint32_t pre = mine + plane * (p.stages * kArrays + (kMode == kSequence ? 2 : 0));
+  auto w_pre = [&](int v) { return kPreShared ? ld_shared_v4(pre + 16u * v * T) : wq[kPreShared ? 0 : v]; };
+  auto factors = [&](int v, F2 (&f)[4]) {
+    if (kPacked) unpack8(kPostShared ? ld_shared_v4(pre + plane + 16u * v * T) : wp[kPostShared ? 0 : v * kPacked], f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = kPacked ? f[j] * both(p.scale) : gw[kPacked ? 0 : v][j];
+  };
   F2 S[V][4], Ppre[V][4];  // kElement: S is this thread's sum for dw_post
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -394,15 +420,26 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
 #pragma unroll
     for (int j = 0; j < 4; ++j) S[v][j] = Ppre[v][j] = both(0.f);
     if (i < p.nv) {
-      unpack8(load_v4(p.w_post + i), gw[v]);
-      wq[v] = load_v4(p.w_pre + i);
+      const uint4 post_w = load_v4(p.w_post + i), pre_w = load_v4(p.w_pre + i);
+      if (kPreShared)
+        ring[(pre - smem_u32(ring)) / 16 + v * T] = pre_w;
+      else
+        wq[kPreShared ? 0 : v] = pre_w;
+      if (kPostShared) {
+        ring[(pre + plane - smem_u32(ring)) / 16 + v * T] = post_w;
+      } else if (kPacked) {
+        wp[kPacked ? v : 0] = post_w;
+      } else {
+        F2(&f)[4] = gw[kPacked ? 0 : v];
+        unpack8(post_w, f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * both(p.scale);
-      if (kMode == kSingle && p.gate) {
-        F2 g[4];
-        unpack8(load_v4(p.gate + i), g);
+        for (int j = 0; j < 4; ++j) f[j] = f[j] * both(p.scale);
+        if (kMode == kSingle && p.gate) {
+          F2 g[4];
+          unpack8(load_v4(p.gate + i), g);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * g[j];
+          for (int j = 0; j < 4; ++j) f[j] = f[j] * g[j];
+        }
       }
       if (kMode == kSequence) store8(post + 8 * v * T, S[v]);
     }
@@ -427,16 +464,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
     for (int v = 0; v < V; ++v) {
       if (t + v * T < p.nv) {
         const uint32_t src = base + 16u * v * T;
-        F2 y[4], x[4], z[4], dh[4], w[4], g[4];
+        F2 y[4], x[4], z[4], dh[4], w[4], g[4], gv[4];
+        factors(v, gv);
         unpack8(ld_shared_v4(src), y);
         unpack8(ld_shared_v4(src + plane), x);
         unpack8(ld_shared_v4(src + 2 * plane), z);
         unpack8(ld_shared_v4(src + 3 * plane), dh);
-        unpack8(wq[v], w);
+        unpack8(w_pre(v), w);
         if (kMode != kSingle) unpack8(ld_shared_v4(src + 4 * plane), g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const F2 br = (kMode != kSingle ? g[j] * gw[v][j] : gw[v][j]) * (y[j] * pn2);
+          const F2 br = (kMode != kSingle ? g[j] * gv[j] : gv[j]) * (y[j] * pn2);
           const F2 rn = (x[j] + br) * qn2;
           const F2 a = dh[j] * w[j];
           Ppre[v][j] = fma2(dh[j], rn, Ppre[v][j]);
@@ -458,19 +496,20 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
     for (int v = 0; v < V; ++v) {
       if (t + v * T < p.nv) {
         const uint32_t src = base + 16u * v * T;
-        F2 yn[4], g[4], dx[4], dy[4];
+        F2 yn[4], g[4], dx[4], dy[4], gv[4];
+        factors(v, gv);
         {
           F2 x[4], dh[4], w[4];
           unpack8(ld_shared_v4(src), yn);
           unpack8(ld_shared_v4(src + plane), x);
           unpack8(ld_shared_v4(src + 2 * plane), dx);
           unpack8(ld_shared_v4(src + 3 * plane), dh);
-          unpack8(wq[v], w);
+          unpack8(w_pre(v), w);
           if (kMode != kSingle) unpack8(ld_shared_v4(src + 4 * plane), g);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             yn[j] = yn[j] * pn2;
-            const F2 f = kMode != kSingle ? g[j] * gw[v][j] : gw[v][j];
+            const F2 f = kMode != kSingle ? g[j] * gv[j] : gv[j];
             const F2 e = fma2(nk1, fma2(f, yn[j], x[j]), dh[j] * w[j]);  // a - rn m1
             dx[j] = fma2(qn2, e, dx[j]);
             dy[j] = fma2(dx[j] * f, pn2, nk2 * yn[j]);
@@ -483,7 +522,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
           for (int j = 0; j < 4; ++j) {
             const F2 ty = dx[j] * yn[j];
             S[v][j] = fma2(g[j], ty, S[v][j]);
-            dx[j] = gw[v][j] * ty;
+            dx[j] = gv[j] * ty;
           }
           p.dgate[at + v * T] = pack8(dx);
         } else {
@@ -495,7 +534,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
           const int i = t + v * T;
           if (first >= m0 && first + p.rows_per_gate <= m1) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dx[j] = gw[v][j] * S[v][j];
+            for (int j = 0; j < 4; ++j) dx[j] = gv[j] * S[v][j];
             p.dgate[gi * p.nv + i] = pack8(dx);
           } else {
             store8(p.part_gate + (2ll * c + (first > m0 ? 1 : 0)) * p.D + 8 * i, S[v]);
@@ -639,7 +678,8 @@ struct Split {
 Split split_of(const gemm_rs_norm_desc* d) {
   Split s;
   const GateMode mode = mode_of(d);
-  s.shape = shape_of((int)(d->D / 8), mode == kSingle ? 4 : 5, d->M, kBlocks, kBackwardSmem, mode == kSequence ? 32 : 0);
+  s.shape = shape_of((int)(d->D / 8), mode == kSingle ? 4 : 5, d->M, kBlocks, kBackwardSmem, mode == kSequence ? 32 : 0,
+                     mode);
   const long long lanes = (long long)kBlocks * s.shape.groups;
   s.chunk_rows = (d->M + lanes - 1) / lanes;
   if (s.chunk_rows < 1) s.chunk_rows = 1;
