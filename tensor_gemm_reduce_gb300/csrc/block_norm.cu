@@ -92,10 +92,10 @@ struct NormParams {
   // backward
   const uint4 *dr, *dh;
   uint4 *dx, *dy, *dgate, *dw_post, *dw_pre;
-  // Rows of a group: `step` = the number of groups apart, so that all blocks
-  // work on one region of memory at a time (8192 x 8192: 101 -> 96 us forward,
-  // 133 -> 127 us backward); in the backward pass with a gate row for some rows
-  // each, chunk_rows consecutive ones (step = 1), whose sums stay in registers.
+  // Rows of a group: chunk_rows consecutive ones (step = 1) where a gate row
+  // serves several of them, else rows `step` = the number of groups apart, so
+  // that all blocks work on one region of memory at a time (8192 x 8192: 101 ->
+  // 96 us forward, 133 -> 127 us backward).
   uint32_t chunk_rows, step;
   int chunks, blocks;
   float *part_post, *part_pre, *part_gate;
@@ -214,24 +214,21 @@ constexpr int forward_blocks(int v) { return v <= 2 ? 2 : 1; }
 // The row stays in the ring until it is written and is unpacked twice: keeping
 // it in registers spilled some of them, and with most of the SM's memory given
 // to the ring every spill went to L2.
-// The gate's row comes through the ring beside x and y, from L2 where it serves
-// several rows; without a gate w_post comes that way, and the registers hold
-// scale alone.  Measured against a gate row (or none) held in registers with
-// w_post, which is loaded again where the next gate row begins: 84.5 against
-// 93.5 us on 8192 x 8192 without a gate, 84.9 against 96.4 with 32 gate rows,
-// 25.4 against 27.7 on 2048 x 8192 with 4, 46.2 against 49.2 on 32768 x 1024;
-// behind only where L2 takes the writes and there is one gate row or none: 25.1
-// against 23.8 on 2048 x 8192, 16.0 against 15.1 on 1024 x 8192.
-template <int V>
+// A gate row that serves several consecutive rows of a group stays in registers
+// with w_post; kGateRing: the gate's row arrives through the ring instead (without
+// a gate w_post does, and the registers hold scale alone).
+template <int V, bool kGateRing>
 __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_kernel(const NormParams p) {
   extern __shared__ uint4 ring[];
   __shared__ float part[2][4][kMaxWarps];
-  constexpr int kArrays = 3;
+  constexpr int kArrays = kGateRing ? 3 : 2;
   const int group = (int)(threadIdx.x >> 5) / p.warps, T = 32 * p.warps;
   const int t = threadIdx.x - group * T;
   const uint32_t mine = smem_u32(ring) + 16u * (group * p.nv + t);
   const uint32_t plane = 16u * p.groups * p.nv;  // one array of a stage
-  const uint32_t m0 = blockIdx.x * p.groups + group, m1 = p.M, step = p.step;
+  const uint32_t c = blockIdx.x * p.groups + group, step = p.step;
+  const uint32_t m0 = step == 1 ? c * p.chunk_rows : c;
+  const uint32_t m1 = step == 1 && m0 + p.chunk_rows < p.M ? m0 + p.chunk_rows : p.M;
   griddep_launch_dependents();  // the next launch's blocks take the places that free up, and wait
   griddep_wait();
 
@@ -239,13 +236,13 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
   auto fetch = [&](uint32_t row, int stage) {
     if (row < m1) {
       const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
-      const uint32_t at = row * p.nv + t, gat = (p.gate ? row / p.rows_per_gate * p.nv : 0) + t;
+      const uint32_t at = row * p.nv + t, gat = (kGateRing && p.gate ? row / p.rows_per_gate * p.nv : 0) + t;
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (t + v * T < p.nv) {
           cp_async16(base + 16u * v * T, p.y + (at + v * T));
           cp_async16(base + plane + 16u * v * T, p.x + (at + v * T));
-          cp_async16(base + 2 * plane + 16u * v * T, factor + (gat + v * T));
+          if (kGateRing) cp_async16(base + 2 * plane + 16u * v * T, factor + (gat + v * T));
         }
     }
     cp_async_commit();
@@ -258,31 +255,46 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
   for (int v = 0; v < V; ++v)
     if (t + v * T < p.nv) w_pre[v * T] = load_v4(p.w_pre + t + v * T);
   F2 gw[V][4];  // the branch's factors that are not in the ring
+  auto branch_weights = [&](uint32_t gate_row) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < V; ++v)
+      if (t + v * T < p.nv) {
+        if (kGateRing && !p.gate) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) gw[v][j] = both(p.scale);
-    if (p.gate && t + v * T < p.nv) {
-      F2 w[4];
-      unpack8(load_v4(p.w_post + t + v * T), w);
+          for (int j = 0; j < 4; ++j) gw[v][j] = both(p.scale);
+          continue;
+        }
+        unpack8(load_v4(p.w_post + t + v * T), gw[v]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) gw[v][j] = w[j] * gw[v][j];
-    }
-  }
+        for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * both(p.scale);
+        if (!kGateRing && p.gate) {
+          F2 g[4];
+          unpack8(load_v4(p.gate + gate_row * p.nv + t + v * T), g);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * g[j];
+        }
+      }
+  };
+  uint32_t gate_row = p.gate ? m0 / p.rows_per_gate : 0, gate_end = p.gate ? (gate_row + 1) * p.rows_per_gate : p.M;
+  if (m0 < p.M) branch_weights(gate_row);
 
   int stage = 0;
   uint32_t it = 0;
 #pragma unroll 1
   for (uint32_t m = m0; m < m1; m += step, ++it) {
+    if (!kGateRing && m == gate_end) {
+      branch_weights(++gate_row);
+      gate_end += p.rows_per_gate;
+    }
     cp_async_wait(p.stages);
     const uint32_t base = mine + (uint32_t)(stage * kArrays) * plane;
     // y, x and the branch c of one vector, from the ring
     auto load = [&](int v, F2 (&y)[4], F2 (&x)[4], F2 (&c)[4]) {
       unpack8(ld_shared_v4(base + 16u * v * T), y);
       unpack8(ld_shared_v4(base + plane + 16u * v * T), x);
-      unpack8(ld_shared_v4(base + 2 * plane + 16u * v * T), c);
+      if (kGateRing) unpack8(ld_shared_v4(base + 2 * plane + 16u * v * T), c);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] = c[j] * gw[v][j] * y[j];
+      for (int j = 0; j < 4; ++j) c[j] = kGateRing ? c[j] * gw[v][j] * y[j] : gw[v][j] * y[j];
     };
     F2 yy = both(0.f), xx = yy, xc = yy, cc = yy;
 #pragma unroll
@@ -407,12 +419,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   uint4 wp[kPacked && !kPostShared ? V : 1], wq[kPreShared ? 1 : V];
   // this thread's vectors of w_pre, after the ring and the columns of dw_post
   const uint32_t pre = mine + plane * (p.stages * kArrays + (kMode == kSequence ? 2 : 0));
-  auto w_pre = [&](int v) { return kPreShared ? ld_shared_v4(pre + 16u * v * T) : wq[kPreShared ? 0 : v]; };
-  auto factors = [&](int v, F2 (&f)[4]) {
-    if (kPacked) unpack8(kPostShared ? ld_shared_v4(pre + plane + 16u * v * T) : wp[kPostShared ? 0 : v * kPacked], f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = kPacked ? f[j] * both(p.scale) : gw[kPacked ? 0 : v][j];
-  };
   F2 S[V][4], Ppre[V][4];  // kElement: S is this thread's sum for dw_post
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -421,30 +427,48 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
     for (int j = 0; j < 4; ++j) S[v][j] = Ppre[v][j] = both(0.f);
     if (i < p.nv) {
       const uint4 post_w = load_v4(p.w_post + i), pre_w = load_v4(p.w_pre + i);
-      if (kPreShared)
+      if constexpr (kPreShared)
         ring[(pre - smem_u32(ring)) / 16 + v * T] = pre_w;
       else
-        wq[kPreShared ? 0 : v] = pre_w;
-      if (kPostShared) {
+        wq[v] = pre_w;
+      if constexpr (kPostShared) {
         ring[(pre + plane - smem_u32(ring)) / 16 + v * T] = post_w;
-      } else if (kPacked) {
-        wp[kPacked ? v : 0] = post_w;
+      } else if constexpr (kPacked) {
+        wp[v] = post_w;
       } else {
-        F2(&f)[4] = gw[kPacked ? 0 : v];
-        unpack8(post_w, f);
+        unpack8(post_w, gw[v]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = f[j] * both(p.scale);
+        for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * both(p.scale);
         if (kMode == kSingle && p.gate) {
           F2 g[4];
           unpack8(load_v4(p.gate + i), g);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = f[j] * g[j];
+          for (int j = 0; j < 4; ++j) gw[v][j] = gw[v][j] * g[j];
         }
       }
       if (kMode == kSequence) store8(post + 8 * v * T, S[v]);
     }
   }
 
+  auto w_pre = [&](int v) {
+    if constexpr (kPreShared)
+      return ld_shared_v4(pre + 16u * v * T);
+    else
+      return wq[v];
+  };
+  auto factors = [&](int v, F2 (&f)[4]) {
+    if constexpr (kPostShared)
+      unpack8(ld_shared_v4(pre + plane + 16u * v * T), f);
+    else if constexpr (kPacked)
+      unpack8(wp[v], f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (kPacked)
+        f[j] = f[j] * both(p.scale);
+      else
+        f[j] = gw[v][j];
+    }
+  };
   int stage = 0;
   // the rows' statistics, one row ahead
   float pn_next = m0 < m1 ? load_f32(p.stats + m0) : 0.f, qn_next = m0 < m1 ? load_f32(p.stats + p.M + m0) : 0.f;
@@ -714,9 +738,10 @@ int launch(const NormParams& p, int grid, int threads, int smem, cudaStream_t st
 }
 
 template <int V>
-int launch_forward(const NormParams& p, int grid, int smem, cudaStream_t st) {
+int launch_forward(const NormParams& p, bool gate_ring, int grid, int smem, cudaStream_t st) {
   const int threads = 32 * p.warps * p.groups;
-  return launch<norm_forward_kernel<V>>(p, grid, threads, smem, st);
+  return gate_ring ? launch<norm_forward_kernel<V, true>>(p, grid, threads, smem, st)
+                    : launch<norm_forward_kernel<V, false>>(p, grid, threads, smem, st);
 }
 template <int V>
 int launch_backward(const NormParams& p, GateMode mode, int smem, cudaStream_t st) {
@@ -747,19 +772,33 @@ extern "C" int gemm_rs_norm_forward(const gemm_rs_norm_desc* d, const void* x, c
   NormParams p = params_of(d);
   p.x = in(x); p.y = in(y); p.gate = in(gate); p.w_post = in(w_post); p.w_pre = in(w_pre);
   p.r = outp(r); p.h = outp(h); p.stats = static_cast<float*>(stats);
-  Shape s = shape_of(p.nv, 3, d->M, 2 * sms, kMaxSmem / 2, 16);
+  // Where the gate's row comes from.  In registers it costs a stall of its group
+  // wherever the next gate row begins, and consecutive rows for each group; through
+  // the ring every row asks L2 for it, which all SMs do for the same lines.  That
+  // pays where gate rows serve under 8 rows, and where rows are whole 128-byte
+  // lines, not short, and there are several gate rows (2048 x 8192 with 4 27.2 ->
+  // 25.2 us, with 128 28.1 -> 25.3; 65536 x 1024 with 4 99.2 -> 92.5; but 20000 x 1000
+  // 31.9 -> 63.9, 131072 x 512 97.4 -> 102.8), or one or none but more traffic than L2
+  // holds (8192 x 8192 94.2 -> 83.3; 2048 x 8192 24.4 -> 25.1): the ring's copies then
+  // pace the reads against the writes.
+  const bool lines = p.nv % 8 == 0 && p.nv >= 128;
+  const bool gate_ring = d->gate_rows > 1 ? lines || p.rows_per_gate < 8 : lines && d->M * p.nv >= (1 << 22);
+  const int arrays = gate_ring ? 3 : 2;
+  Shape s = shape_of(p.nv, arrays, d->M, 2 * sms, kMaxSmem / 2, 16);
   const int per_sm = forward_blocks(s.v);
-  if (per_sm == 1) s = shape_of(p.nv, 3, d->M, sms, kMaxSmem, 16);
+  if (per_sm == 1) s = shape_of(p.nv, arrays, d->M, sms, kMaxSmem, 16);
   set_shape(&p, s);
-  const long long rows = ((long long)d->M + s.groups - 1) / s.groups;  // of a block's groups together
-  const int grid = (int)(rows < (long long)per_sm * sms ? rows : (long long)per_sm * sms);
-  p.step = (uint32_t)(grid * s.groups);
+  const long long lanes = (long long)per_sm * sms * s.groups;
+  p.chunk_rows = (uint32_t)((d->M + lanes - 1) / lanes);
+  const long long chunks = (d->M + p.chunk_rows - 1) / p.chunk_rows;
+  const int grid = (int)((chunks + s.groups - 1) / s.groups);
+  p.step = d->gate_rows > 1 && !gate_ring ? 1 : (uint32_t)(grid * s.groups);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (s.v) {
-    case 1: return launch_forward<1>(p, grid, s.smem, st);
-    case 2: return launch_forward<2>(p, grid, s.smem, st);
-    case 3: return launch_forward<3>(p, grid, s.smem, st);
-    default: return launch_forward<4>(p, grid, s.smem, st);
+    case 1: return launch_forward<1>(p, gate_ring, grid, s.smem, st);
+    case 2: return launch_forward<2>(p, gate_ring, grid, s.smem, st);
+    case 3: return launch_forward<3>(p, gate_ring, grid, s.smem, st);
+    default: return launch_forward<4>(p, gate_ring, grid, s.smem, st);
   }
 }
 

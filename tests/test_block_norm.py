@@ -94,11 +94,13 @@ def assert_close(got, ref, mag, steps, name):
                            f"{np.nanmax(np.abs(got - ref) / bound):.2f} x the bound")
 
 
-# rows and columns at the edges: one row, one vector, a ragged last warp, two to four vectors a thread,
-# fewer and more rows than chunks, gate rows that divide, straddle and equal the chunks
+# rows and columns at the edges: one row, one vector, a ragged last warp, two to four vectors a thread, fewer and
+# more rows than chunks, gate rows that divide, straddle and equal the chunks; gate rows of 7 and 8 rows and rows of
+# whole 128-byte lines, where the gate's way into the forward kernel changes
 SHAPES = [(1, 8, 0), (1, 8, 1), (3, 64, 3), (2, 264, 2), (5, 1000, 1), (1, 8192, 1), (152, 512, 8), (153, 520, 3),
           (304, 768, 4), (610, 256, 5), (700, 128, 350), (1003, 136, 1003), (960, 72, 6), (17, 4104, 0),
-          (9, 8200, 3), (6, 12288, 2), (4, 12296, 1), (5, 16384, 5), (6, 16384, 2), (1520, 1032, 10), (2048, 520, 256), (1050, 264, 150)]
+          (9, 8200, 3), (6, 12288, 2), (4, 12296, 1), (5, 16384, 5), (6, 16384, 2), (1520, 1032, 10), (2048, 520, 256), (1050, 264, 150),
+          (96, 1024, 4), (1200, 1024, 3), (40, 4160, 2), (310, 1088, 10)]
 
 
 @pytest.mark.gpu
@@ -114,6 +116,25 @@ def test_forward_matches_the_formula(M, D, gate_rows, scale):
     assert_close(r, f["r"], mag, 256, "r")
     assert_close(h, f["h"], mag * f["q"] * np.abs(w_pre), 256, "h")
     np.testing.assert_allclose(f64(stats), np.stack([f["p"][:, 0], f["q"][:, 0]]), rtol=256 * U)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate_rows", [0, 1])
+def test_forward_of_many_rows(gate_rows):
+    """More traffic than L2 holds: some rows against the formula, which is a row's own."""
+    M, D, scale = 4100, 8192, 0.6
+    gen = torch.Generator("cuda").manual_seed(3)
+    x, y = (torch.randn(M, D, device="cuda", generator=gen).bfloat16() for _ in range(2))
+    t = inputs(1, D, gate_rows, seed=5)
+    d = dev(t)
+    r, h, stats = block_norm.forward(x, y, d["w_post"], d["w_pre"], gate=d["gate"], scale=scale, eps=1e-6)
+    rows = torch.tensor([0, 1, 151, 152, 303, 304, 2047, 2048, 4095, 4099], device="cuda")
+    xs, ys, w_post, w_pre, gate = f64(x[rows]), f64(y[rows]), f64(t["w_post"]), f64(t["w_pre"]), f64(t["gate"])
+    f = reference(xs, ys, w_post, w_pre, gate, scale, 1e-6)
+    mag = np.abs(xs) + np.abs(f["c"])
+    assert_close(r[rows], f["r"], mag, 256, "r")
+    assert_close(h[rows], f["h"], mag * f["q"] * np.abs(w_pre), 256, "h")
+    np.testing.assert_allclose(f64(stats[:, rows]), np.stack([f["p"][:, 0], f["q"][:, 0]]), rtol=256 * U)
 
 
 @pytest.mark.gpu
