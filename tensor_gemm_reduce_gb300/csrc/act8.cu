@@ -6,7 +6,10 @@
 // rebuilds two elements at a time with bf16x2 arithmetic, all of it exact.
 // The four bytes of a word hold elements 0, 2, 1, 3: the low bytes of its
 // 16-bit halves are elements 0 and 1, the high ones 2 and 3.
-// Both kernels move 3.03 bytes an element and are bound by HBM.
+// Both kernels move 3.03 bytes an element and are bound by HBM: the two together take
+// 214 us for 8192 x 28672 (1.42 GB, 6.64 TB/s, a copy's rate is 6.79) and 15.3 us for
+// 512 x 28672 (5.8 TB/s).  Plain 16-byte loads, four in flight a thread and enough
+// threads on each SM, reach that without shared memory.
 #include "act8.cuh"
 #include "ops_common.cuh"
 
