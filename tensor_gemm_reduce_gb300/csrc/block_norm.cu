@@ -611,20 +611,57 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   }
 }
 
+// The chunks whose sums make up a gate row that crosses a chunk border: job j's
+// gate row, or false if it has none.  Gate row j if there are fewer gate rows than
+// chunks, else the one that crosses the border after chunk j as its first.
+struct GateChunks {
+  long long gi, first;  // the gate row, its first chunk
+  int n;
+  bool odd;  // the first chunk's slot (the later chunks' are even)
+};
+__device__ __forceinline__ bool gate_chunks(const NormParams& p, int j, int by_gate, GateChunks* g) {
+  g->gi = by_gate ? j : (long long)(j + 1) * p.chunk_rows / p.rows_per_gate;
+  const long long first = g->gi * p.rows_per_gate, last = first + p.rows_per_gate - 1;
+  g->first = first / p.chunk_rows;
+  if (last / p.chunk_rows == g->first || (!by_gate && g->first != j)) return false;
+  g->n = (int)(last / p.chunk_rows - g->first) + 1;
+  g->odd = first > g->first * p.chunk_rows;
+  return true;
+}
+
 // Joins the blocks' sums, 128 columns a block: warp w adds rows w, w + 16, ...,
 // four columns a lane and all of its rows' loads in flight at once, and the
 // sixteen sums are added in order.  blockIdx.y: 0 dw_pre, 1 dw_post (and dgate
-// when there is one gate row), from 2 on the gate rows that cross a chunk border:
-// gate row blockIdx.y - 2 if there are fewer gate rows than chunks, else the one
-// that crosses the border after chunk blockIdx.y - 2 as its first.
+// when there is one gate row), from 2 on the gate rows that cross a chunk border.
+// Those that at most kJoinWarps chunks share (warp_each) take a warp each, which
+// adds the chunks' sums in order (127 gate rows that two chunks share, 8192
+// columns: a block each 88 us, a warp 13.5).
 constexpr int kJoinWarps = 16, kJoinCols = 128;
-__global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const NormParams p, int many_gates, int by_gate) {
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    norm_join_kernel(const NormParams p, int many_gates, int by_gate, int gate_jobs, int warp_each) {
   __shared__ float part[kJoinWarps][kJoinCols];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * kJoinCols + 4 * lane;
   const int job = blockIdx.y;
   griddep_launch_dependents();
   griddep_wait();
+  GateChunks g;
+  if (job >= 2 && warp_each) {
+    const int j = (job - 2) * kJoinWarps + warp;
+    if (j >= gate_jobs || col >= p.D || !gate_chunks(p, j, by_gate, &g)) return;
+    const float* src = p.part_gate + 2 * g.first * p.D + col;
+    F2 lo = both(0.f), hi = lo;
+#pragma unroll 4
+    for (int k = 0; k < g.n; ++k) {
+      const uint4 v = load_v4_stream(src + 2ll * k * p.D + (g.odd && k == 0 ? p.D : 0));
+      lo = lo + f2(__uint_as_float(v.x), __uint_as_float(v.y));
+      hi = hi + f2(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    const uint2 w = load_v2_stream(reinterpret_cast<const uint16_t*>(p.w_post) + col);
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.dgate) + g.gi * p.D + col) =
+        make_uint2(to_bf16x2(both(p.scale) * from_bf16x2(w.x) * lo), to_bf16x2(both(p.scale) * from_bf16x2(w.y) * hi));
+    return;
+  }
   const float* src;
   int n = p.blocks;  // rows of src to add, `step` apart
   long long step = p.D, gi = 0;
@@ -634,14 +671,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const NormPa
   } else if (job == 1) {
     src = p.part_post;
   } else {
-    gi = by_gate ? job - 2 : (long long)(job - 1) * p.chunk_rows / p.rows_per_gate;
-    const long long first = gi * p.rows_per_gate, last = first + p.rows_per_gate - 1;
-    const long long b = first / p.chunk_rows;
-    if (last / p.chunk_rows == b || (!by_gate && b != job - 2)) return;
-    n = (int)(last / p.chunk_rows - b) + 1;
-    src = p.part_gate + 2 * b * p.D;
+    if (!gate_chunks(p, job - 2, by_gate, &g)) return;
+    gi = g.gi;
+    n = g.n;
+    src = p.part_gate + 2 * g.first * p.D;
     step = 2ll * p.D;
-    odd = first > b * p.chunk_rows;  // chunk b's slot; the later chunks' are even
+    odd = g.odd;
   }
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kBatch = (kBlocks + kJoinWarps - 1) / kJoinWarps;
@@ -874,8 +909,10 @@ extern "C" int gemm_rs_norm_backward(const gemm_rs_norm_desc* d, const void* dr,
   }
   if (rc) return rc;
   const int many_gates = mode != kSingle, by_gate = d->gate_rows < sp.chunks;
-  const long long crossing = mode != kSequence ? 0 : by_gate ? d->gate_rows : sp.chunks - 1;
-  return launch_overlapped(norm_join_kernel, dim3((unsigned)((p.D + kJoinCols - 1) / kJoinCols), (unsigned)(2 + crossing)),
-                           32 * kJoinWarps, 0, st, p,
-                           many_gates, by_gate);
+  const int crossing = (int)(mode != kSequence ? 0 : by_gate ? d->gate_rows : sp.chunks - 1);
+  const int warp_each = p.rows_per_gate / sp.chunk_rows + 2 <= kJoinWarps;  // chunks of a gate row, at most
+  return launch_overlapped(norm_join_kernel,
+                           dim3((unsigned)((p.D + kJoinCols - 1) / kJoinCols),
+                                (unsigned)(2 + (warp_each ? (crossing + kJoinWarps - 1) / kJoinWarps : crossing))),
+                           32 * kJoinWarps, 0, st, p, many_gates, by_gate, crossing, warp_each);
 }

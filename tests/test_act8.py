@@ -138,7 +138,8 @@ def run(M, N, K, A, W, dY, da=True, dw=True, plan=None, ws=None):
 
 # one token row block, ragged in every dimension, several tiles, single steps, more tiles than pairs
 PROBLEMS = [(8, 8, 64), (8, 264, 512), (128, 512, 1024), (392, 776, 1600), (264, 1032, 2112), (72, 2056, 4160),
-            (512, 136, 8192), (1040, 520, 576), (256, 4096, 2048), (8, 64, 24576 + 64)]
+            (512, 136, 8192), (1040, 520, 576), (256, 4096, 2048), (8, 64, 24576 + 64), (136, 392, 2624), (80, 712, 1216),
+            (328, 1144, 448)]
 
 
 @pytest.mark.gpu
