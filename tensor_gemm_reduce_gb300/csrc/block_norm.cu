@@ -94,6 +94,7 @@ struct NormParams {
   int warps, groups, stages;
   uint32_t rows_per_gate;   // M / gate_rows
   float scale, eps, inv_d;
+  float least, least_eps;   // D 2^-124, and that less D eps
   const uint4 *x, *y, *gate, *w_post, *w_pre;
   uint4 *r, *h;
   float* stats;
@@ -216,9 +217,13 @@ constexpr int forward_blocks(int v) { return v <= 2 ? 2 : 1; }
 
 // With c = scale gate w_post y the row's residual is r = x + p c, so
 //   sum r^2 = sum x^2 + 2 p sum x c + p^2 sum c^2
-// and one sum of four values (y^2, x^2, x c, c^2) serves both norms.  Where the
-// branch cancels most of x (the result is under a quarter of the positive
-// terms) the rounding of the terms would show, and sum r^2 is taken directly.
+// and one sum of four values (y^2, x^2, x c, c^2) serves both norms.  sum r^2 is
+// taken directly where it would not have its digits:
+//   sum r^2 + D eps < (terms that are not negative) / 4 + D 2^-124 (1 + p^2)
+// The first part is a branch that cancels most of x, where the rounding of the terms
+// would show; the second are products below 2^-126, each off by 2^-150 and multiplied
+// by up to 1 + p^2.  An overflowing term or p^2 leaves NaN or infinity in the
+// comparison, which does not hold then either.
 // The row stays in the ring until it is written and is unpacked twice: keeping
 // it in registers spilled some of them, and with most of the SM's memory given
 // to the ring every spill went to L2.
@@ -324,7 +329,8 @@ __global__ void __launch_bounds__(kMaxThreads, forward_blocks(V)) norm_forward_k
     const F2 pn2 = both(pn);
     const float terms = fmaf(pn * pn, s[3], s[1]);
     float rr = fmaf(2.f * pn, s[2], terms);
-    if (!(rr >= 0.25f * terms)) {  // the same in every thread of the group; also for an infinite term
+    // the same in every thread of the group
+    if (!(fmaf(-0.25f, terms, rr) >= fmaf(pn * pn, p.least, p.least_eps))) {
       F2 acc = both(0.f);
 #pragma unroll
       for (int v = 0; v < V; ++v)
@@ -764,6 +770,8 @@ NormParams params_of(const gemm_rs_norm_desc* d) {
   p.scale = d->scale;
   p.eps = d->eps;
   p.inv_d = 1.f / (float)d->D;
+  p.least = 0x1p-124f * (float)d->D;
+  p.least_eps = p.least - d->eps * (float)d->D;
   return p;
 }
 

@@ -219,6 +219,41 @@ def test_a_branch_that_cancels_the_residual(left):
                  256, "h")
 
 
+# (size of y, of the branch's factor, of x, eps): sum c^2 and sum x c overflow before p brings them back, c = factor y;
+# p^2 overflows; c^2 is below the smallest number, and it is all there is of r
+FAR = [(3e16, 16.0, 1.0, 1e-6), (3e16, -16.0, 0.0, 1e-6), (2e16, 64.0, 30.0, 0.0), (2e-20, 3.0, 1.0, 0.0),
+       (1e-18, 1e-6, 0.0, 0.0), (1e-18, 1e-6, 1e-6, 0.0)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,D,gate_rows", [(3, 8192, 1), (4, 264, 2), (3, 72, 3), (2, 12288, 0), (16, 1024, 2)])
+@pytest.mark.parametrize("size,factor,x_size,eps", FAR)
+def test_a_branch_whose_square_leaves_the_range(M, D, gate_rows, size, factor, x_size, eps):
+    """r and its root are of ordinary size, y and the terms of sum r^2 are not.  Products below the
+    smallest normal number are off by 2**-150 each: 1e-5 of the 4e-40 that a square of y is at least."""
+    rng = np.random.default_rng(D)
+    t = inputs(M, D, gate_rows, seed=D)
+    signs = rng.choice([-1.0, 1.0], (M, D))
+    t["y"] = torch.from_numpy(size * signs * rng.uniform(1, 4, (M, D))).to(torch.bfloat16)
+    t["x"] = torch.from_numpy(x_size * rng.standard_normal((M, D))).to(torch.bfloat16)
+    scale = 0.5 * factor
+    if gate_rows:
+        t["gate"] = torch.from_numpy(rng.uniform(1.5, 2.5, (gate_rows, D))).to(torch.bfloat16)
+    d = dev(t)
+    args = (d["x"], d["y"], d["w_post"], d["w_pre"])
+    r, h, stats = block_norm.forward(*args, gate=d["gate"], scale=scale, eps=eps)
+    host = [f64(t[k]) for k in ("x", "y", "w_post", "w_pre", "gate")]
+    f = reference(*host, scale, eps)
+    mag = np.abs(host[0]) + np.abs(f["c"])
+    assert_close(r, f["r"], mag, 256, "r")
+    assert_close(h, f["h"], mag * f["q"] * np.abs(host[3]), 256, "h")
+    np.testing.assert_allclose(f64(stats), np.stack([f["p"][:, 0], f["q"][:, 0]]), rtol=256 * U)
+    got = block_norm.backward(d["dr"], d["dh"], *args, stats, gate=d["gate"], scale=scale)
+    ref = reference_grads(f64(t["dr"]), f64(t["dh"]), *host, scale, eps)
+    assert_close(got[0], *ref["dx"], 256, "dx")
+    assert_close(got[3], *ref["dw_pre"], 256 + M + 160, "dw_pre")
+
+
 @pytest.mark.gpu
 def test_rows_with_nothing_or_not_finite_stay_alone():
     """A zero row (eps alone in the root), an infinite and a NaN value change their own rows only."""
