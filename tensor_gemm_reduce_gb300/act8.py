@@ -9,6 +9,8 @@ gemm_rs_bwd_* in include/gemm_rs_ops.h).
 32 consecutive elements of a row share a power of two, the least that holds
 the largest of them in 7 bits and a sign; a restored value is exact in bf16.
 A group with an infinity or a NaN is restored as NaN.
+
+Calls run on `stream`, or the current one, and what they allocate belongs to it.
 """
 from __future__ import annotations
 
@@ -46,7 +48,8 @@ def save(A, out: Checkpoint = None, stream=None) -> Checkpoint:
     if A.dim() != 3 or A.shape[0] != _a.WORLD:
         raise ValueError(f"A must have shape [{_a.WORLD}][M][K/{_a.WORLD}], got {tuple(A.shape)}")
     if out is None:
-        out = Checkpoint(A.shape[1], A.shape[2] * _a.WORLD, A.device)
+        with _a.allocating_for(stream):
+            out = Checkpoint(A.shape[1], A.shape[2] * _a.WORLD, A.device)
     elif out.shape != A.shape:
         raise ValueError(f"the checkpoint holds {tuple(out.shape)}, A is {tuple(A.shape)}")
     rc = _a.ops().act8(A, out.codes, out.scales, False, None if stream is None else stream.cuda_stream)
@@ -58,7 +61,8 @@ def save(A, out: Checkpoint = None, stream=None) -> Checkpoint:
 def restore(ck: Checkpoint, out=None, stream=None):
     """The bf16 values [8][M][K/8] that a checkpoint stands for."""
     if out is None:
-        out = torch.empty(ck.shape, dtype=_BF16, device=ck.codes.device)
+        with _a.allocating_for(stream):
+            out = torch.empty(ck.shape, dtype=_BF16, device=ck.codes.device)
     elif out.shape != ck.shape:
         raise ValueError(f"the checkpoint holds {tuple(ck.shape)}, out is {tuple(out.shape)}")
     rc = _a.ops().act8(out, ck.codes, ck.scales, True, None if stream is None else stream.cuda_stream)

@@ -8,6 +8,8 @@ and residual scale (binding of gemm_rs_norm_* in include/gemm_rs_ops.h).
 x, y, r, h: [M][D] bf16; w_post, w_pre: [D] bf16; gate: [G][D] bf16 or None,
 its row i serving rows [i*M/G, (i+1)*M/G); rms(v) = sqrt(mean(v^2) + eps).
 D is a multiple of 8, at most 16384.  Arithmetic is fp32, rounded once.
+
+Calls run on `stream`, or the current one, and what they allocate belongs to it.
 """
 from __future__ import annotations
 
@@ -59,7 +61,10 @@ def new_workspace(x, gate=None):
 
 def forward(x, y, w_post, w_pre, gate=None, scale: float = 1.0, eps: float = 1e-6, out=None, stream=None):
     """Returns (r, h, stats); `out` takes the tensors of new_outputs()."""
-    r, h, stats = out if out is not None else new_outputs(x)
+    if out is None:
+        with _a.allocating_for(stream):
+            out = new_outputs(x)
+    r, h, stats = out
     rc = _a.ops().norm_forward(x, y, w_post, w_pre, gate, scale, eps, r, h, stats,
                                None if stream is None else stream.cuda_stream)
     if rc:
@@ -72,9 +77,11 @@ def backward(dr, dh, x, y, w_post, w_pre, stats, gate=None, scale: float = 1.0, 
     """Gradients (dx, dy, dw_post, dw_pre, dgate) for dr and dh, the gradients of
     forward()'s r and h; stats as forward() returned them; dgate is None without
     a gate.  `out` takes the tensors of new_gradients()."""
-    dx, dy, dw_post, dw_pre, dgate = out if out is not None else new_gradients(x, gate)
-    if workspace is None:
-        workspace = new_workspace(x, gate)
+    if out is None or workspace is None:
+        with _a.allocating_for(stream):
+            out = new_gradients(x, gate) if out is None else out
+            workspace = new_workspace(x, gate) if workspace is None else workspace
+    dx, dy, dw_post, dw_pre, dgate = out
     rc = _a.ops().norm_backward(dr, dh, x, y, w_post, w_pre, gate, stats, scale, dx, dy, dw_post, dw_pre, dgate,
                                 workspace, None if stream is None else stream.cuda_stream)
     if rc:

@@ -10,6 +10,7 @@ operators run.  What is called once (layouts, plans, packing) uses ctypes.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -94,6 +95,17 @@ def header_symbols():
 def check(rc: int, what: str) -> None:
     if rc != _g.GEMM_RS_OK:
         raise GemmRSError(rc, what)
+
+
+_AS_IT_IS = contextlib.nullcontext()
+
+
+def allocating_for(stream):
+    """Context for what a call allocates when it runs on `stream`: the memory then belongs
+    to that stream.  From the current stream's memory a call could be given a block that
+    this stream's earlier work still reads, and a temporary that the call drops could go to
+    the current stream's next allocation before `stream` has used it."""
+    return _AS_IT_IS if stream is None else torch.cuda.stream(stream)
 
 
 def pointer(t, shape, dtype, name: str) -> int:

@@ -9,6 +9,8 @@ scales (binding of gemm_rs_w4_* in include/gemm_rs_ops.h).
 x [8][M][K/8] bf16, codes [8][K/8][N] uint8 (0..15), scales and zeros
 [8][ceil(K/8/group)][N] bf16 and uint8; without zeros 8 is subtracted.
 quantize() makes symmetric codes of a bf16 weight.
+
+Calls run on `stream`, or the current one, and what they allocate belongs to it.
 """
 from __future__ import annotations
 
@@ -45,8 +47,9 @@ def quantize(W, group: int = 128, stream=None):
         raise ValueError(f"W must have shape [{_a.WORLD}][K/{_a.WORLD}][N], got {tuple(W.shape)}")
     _, Kr, N = W.shape
     w = _a.pointer(W, W.shape, _BF16, "W")
-    codes = torch.empty(W.shape, dtype=_U8, device=W.device)
-    scales = torch.empty(_a.WORLD, _groups(Kr, group), N, dtype=_BF16, device=W.device)
+    with _a.allocating_for(stream):
+        codes = torch.empty(W.shape, dtype=_U8, device=W.device)
+        scales = torch.empty(_a.WORLD, _groups(Kr, group), N, dtype=_BF16, device=W.device)
     _a.check(_a.lib().gemm_rs_w4_quantize(N, Kr * _a.WORLD, group, w, codes.data_ptr(), scales.data_ptr(),
                                           _a.stream_handle(stream, W.device)), "gemm_rs_w4_quantize")
     return codes, scales
@@ -61,7 +64,8 @@ def pack(codes, scales, zeros=None, group: int = 128, stream=None) -> Weight:
     c = _a.pointer(codes, codes.shape, _U8, "codes")
     s = _a.pointer(scales, per_group, _BF16, "scales")
     z = None if zeros is None else _a.pointer(zeros, per_group, _U8, "zeros")
-    weight = Weight(N, Kr * _a.WORLD, group, zeros is not None, codes.device)
+    with _a.allocating_for(stream):
+        weight = Weight(N, Kr * _a.WORLD, group, zeros is not None, codes.device)
     _a.check(_a.lib().gemm_rs_w4_pack(N, weight.K, group, c, s, z, weight.data.data_ptr(),
                                       _a.stream_handle(stream, codes.device)), "gemm_rs_w4_pack")
     return weight
@@ -78,7 +82,8 @@ def matvec(x, weight: Weight, out=None, workspace=None, stream=None):
     if out is None:
         if x.dim() != 3:
             raise ValueError(f"x must have shape [{_a.WORLD}][M][K/{_a.WORLD}], got {tuple(x.shape)}")
-        out = torch.empty(x.shape[1], weight.N, dtype=_BF16, device=x.device)
+        with _a.allocating_for(stream):
+            out = torch.empty(x.shape[1], weight.N, dtype=_BF16, device=x.device)
     rc = _a.ops().w4_matvec(x, weight.N, weight.K, weight.group, weight.has_zeros, weight.data, out,
                             None if stream is None else stream.cuda_stream)
     if rc:
