@@ -100,12 +100,14 @@ typedef struct gemm_rs_bwd_plan_s* gemm_rs_bwd_t;
  * before any CUDA call.  N % 8 == 0, the others as above. */
 int gemm_rs_bwd_create(int64_t M, int64_t N, int64_t K, uint64_t timeout_ns, gemm_rs_bwd_t* plan,
                        size_t* workspace_bytes);
-/* The workspace may be uninitialised; the first call that sees a new pointer
- * clears the control words at its end.  A plan serves one stream at a time. */
+/* The workspace needs no initialisation, and plans that follow one another on a
+ * stream may share one.  It stays allocated until the run's status has been
+ * asked for, or never is.  A plan serves one stream at a time. */
 int gemm_rs_bwd_run(gemm_rs_bwd_t plan, const void* dY, const void* W, const void* codes,
                     const void* scales, void* dA, void* dW, void* workspace, void* stream);
-/* Synchronises `stream`; GEMM_RS_OK, GEMM_RS_ERR_TIMEOUT (a device-side wait
- * gave up, the outputs are incomplete) or GEMM_RS_ERR_CUDA. */
+/* Status of the last run in the plan's last workspace, which it reads and does not
+ * change.  Synchronises `stream`; GEMM_RS_OK, GEMM_RS_ERR_TIMEOUT (a device-side
+ * wait gave up, the outputs are incomplete) or GEMM_RS_ERR_CUDA. */
 int gemm_rs_bwd_status(gemm_rs_bwd_t plan, void* stream);
 int gemm_rs_bwd_destroy(gemm_rs_bwd_t plan);
 

@@ -80,7 +80,7 @@ class BackwardPlan:
         h, ws = ctypes.c_void_p(), ctypes.c_size_t()
         _a.check(_a.lib().gemm_rs_bwd_create(self.M, self.N, self.K, timeout_ns, ctypes.byref(h),
                                              ctypes.byref(ws)), "gemm_rs_bwd_create")
-        self._h, self.workspace_bytes = h.value, ws.value
+        self._h, self.workspace_bytes, self._workspace = h.value, ws.value, None
         Kr = self.K // _a.WORLD
         self.a_shape = torch.Size((_a.WORLD, self.M, Kr))
         self.w_shape = torch.Size((_a.WORLD, Kr, self.N))
@@ -101,16 +101,18 @@ class BackwardPlan:
                                workspace, None if stream is None else stream.cuda_stream)
         if rc:
             _a.check(rc, "gemm_rs_bwd_run")
+        self._workspace = workspace  # status() reads it
 
     def status(self, stream=None) -> int:
-        """Synchronise the stream and report the device-side status of the last run."""
+        """Synchronise the stream and report the device-side status of the last run, whose
+        workspace the plan keeps for this until its next run or close()."""
         s = stream if stream is not None else torch.cuda.current_stream()
         return _a.lib().gemm_rs_bwd_status(self._h, s.cuda_stream)
 
     def close(self):
         if getattr(self, "_h", None):
             _a.lib().gemm_rs_bwd_destroy(self._h)
-            self._h = None
+            self._h = self._workspace = None
 
     def __del__(self):
         try:

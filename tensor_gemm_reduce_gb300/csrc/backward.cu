@@ -18,8 +18,9 @@
 // library product sustains and 0.86 of its burst; 512 x 8192 x 28672 334 to 340 us,
 // 1.42 PFLOP/s (its dW tiles contract over 8 steps, so what a tile costs besides,
 // 500 to 1000 cycles, and 1 GB of operands and outputs weigh more).
-// Every wait is bounded; on expiry the kernel records an error word, lets its
-// copies land, frees TMEM and returns.
+// Every wait is bounded; on expiry the kernel lets its copies land, frees TMEM and
+// returns.  Each CTA says at its end, in a word of its own, whether it gave up, so
+// nothing has to be cleared before a run, whatever the workspace held.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -52,6 +53,10 @@ static_assert(kSmemAlloc <= 232448, "shared memory per CTA");
 // 12928 16.0 -> 17.0, 1000 x 1032 x 6400 35.8 -> 37.1, the largest no difference).
 constexpr int64_t kRestoreBeside = 2 << 20;
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+// The workspace: a status word for each CTA, then the restored activations.  The words
+// come first so that plans of any sizes which share a workspace agree on the place.
+constexpr int kStatusWords = 256;
+constexpr size_t kStatusBytes = kStatusWords * sizeof(uint32_t);
 
 // One of the two products: 8 ranks of mt x nt tiles, kb steps of kBK each.
 struct Product {
@@ -115,7 +120,7 @@ struct BwdParams {
   CUtensorMap dy_k, w_k, a_mn, dy_mn, out_da, out_dw;
   Schedule s;
   int M, N, Kr;
-  uint32_t* error;  // [0] non-zero once a wait gave up
+  uint32_t* status;  // [CTA] written at its end: non-zero if a wait gave up
   int restored_before;  // the launch before this one restores A and lets this one start early
   unsigned long long timeout_ns;
 };
@@ -133,11 +138,6 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t
       if (probe()) return true;
     if (*cta_abort || globaltimer_ns() - t0 > limit_ns) return false;
   }
-}
-
-__device__ __forceinline__ void give_up(const BwdParams& p, volatile uint32_t* cta_abort) {
-  if (!*cta_abort) atomicExch(p.error, 1u);
-  *cta_abort = 1;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
@@ -208,7 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
         const int x0 = (is_a ? t.mt : t.nt) * kTile + cta * 128;
         for (int kb = 0; kb < kb_count; ++kb) {
           if (!wait_bar(bar_empty + 8 * stage, phase ^ 1u, limit, cta_abort)) {
-            give_up(p, cta_abort);
+            *cta_abort = 1;
             ok = false;
             break;
           }
@@ -255,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
       bool ok = true;
       while (ok && walk.next(p.s, &t)) {
         if (!wait_bar(bar_acc_empty + 8 * acc, acc_phase ^ 1u, limit, cta_abort, true)) {
-          give_up(p, cta_abort);
+          *cta_abort = 1;
           break;
         }
         tc_fence_after();
@@ -266,7 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
         const int kb_count = t.is_dw ? p.s.dw.kb : p.s.da.kb;
         for (int kb = 0; kb < kb_count; ++kb) {
           if (!wait_bar(bar_full + 8 * stage, phase, limit, cta_abort)) {
-            give_up(p, cta_abort);
+            *cta_abort = 1;
             ok = false;
             break;
           }
@@ -304,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
       if (lane == 0) got = wait_bar(bar_acc_full + 8 * acc, acc_phase, limit, cta_abort) ? 1 : 0;
       got = __shfl_sync(0xffffffffu, got, 0);
       if (!got) {
-        if (lane == 0) give_up(p, cta_abort);
+        if (lane == 0) *cta_abort = 1;
         break;
       }
       tc_fence_after();
@@ -365,6 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) p.status[blockIdx.x] = *cta_abort;
   cluster_sync();  // no MMA or remote arrival targets this CTA any more
   if (warp == 1) {
     tc_fence_after();
@@ -441,8 +442,9 @@ struct gemm_rs_bwd_plan_s {
   int64_t M, N, K, Kr;
   uint64_t timeout_ns;
   int max_pairs;
-  size_t a_bytes, total;
-  void* last_ws = nullptr;
+  size_t total;
+  const void* last_ws = nullptr;  // of the last run; null if it launched no kernel
+  int last_ctas = 0;
 };
 
 extern "C" int gemm_rs_bwd_create(int64_t M, int64_t N, int64_t K, uint64_t timeout_ns, gemm_rs_bwd_t* plan,
@@ -483,8 +485,8 @@ extern "C" int gemm_rs_bwd_create(int64_t M, int64_t N, int64_t K, uint64_t time
   h->Kr = Kr;
   h->timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
   h->max_pairs = pairs < sms / 2 ? pairs : sms / 2;
-  h->a_bytes = (size_t)kWorld * M * act8_pitch(Kr) * 2;  // whole 256-byte lines: TMA reads boxes of 128
-  h->total = h->a_bytes + 256;
+  if (h->max_pairs > kStatusWords / 2) h->max_pairs = kStatusWords / 2;
+  h->total = kStatusBytes + (size_t)kWorld * M * act8_pitch(Kr) * 2;  // whole 256-byte lines: TMA reads boxes of 128
   if (workspace_bytes) *workspace_bytes = h->total;
   *plan = h;
   return GEMM_RS_OK;
@@ -495,7 +497,10 @@ extern "C" int gemm_rs_bwd_run(gemm_rs_bwd_t h, const void* dY, const void* W, c
   if (!h) return GEMM_RS_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool da = dA && h->M > 0 && h->Kr > 0, dw = dW && h->N > 0 && h->Kr > 0;
-  if (!da && !dw) return GEMM_RS_OK;
+  if (!da && !dw) {
+    h->last_ws = nullptr;
+    return GEMM_RS_OK;
+  }
   if (h->M > 0 && h->N > 0 && (!dY || (da && !W) || (dw && (!codes || !scales)))) return GEMM_RS_ERR_INVALID_ARG;
   for (const void* q : {dY, W, codes, scales, (const void*)dA, (const void*)dW, (const void*)workspace})
     if (misaligned16(q)) return GEMM_RS_ERR_MISALIGNED;
@@ -503,20 +508,17 @@ extern "C" int gemm_rs_bwd_run(gemm_rs_bwd_t h, const void* dY, const void* W, c
   if (h->M == 0 || h->N == 0) {  // an empty contraction
     void* out = h->M == 0 ? dW : dA;
     const size_t bytes = (size_t)kWorld * h->Kr * (h->M == 0 ? h->N : h->M) * 2;
-    if (cudaMemsetAsync(out, 0, bytes, st) == cudaSuccess) return GEMM_RS_OK;
-    cudaGetLastError();
-    return GEMM_RS_ERR_CUDA;
-  }
-  BwdParams p;
-  memset(&p, 0, sizeof(p));
-  p.error = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + h->a_bytes);
-  if (h->last_ws != workspace) {
-    if (cudaMemsetAsync(p.error, 0, 256, st) != cudaSuccess) {
+    if (cudaMemsetAsync(out, 0, bytes, st) != cudaSuccess) {
       cudaGetLastError();
       return GEMM_RS_ERR_CUDA;
     }
-    h->last_ws = workspace;
+    h->last_ws = nullptr;
+    return GEMM_RS_OK;
   }
+  BwdParams p;
+  memset(&p, 0, sizeof(p));
+  p.status = static_cast<uint32_t*>(workspace);
+  void* const restored = static_cast<uint8_t*>(workspace) + kStatusBytes;
   p.M = (int)h->M;
   p.N = (int)h->N;
   p.Kr = (int)h->Kr;
@@ -527,39 +529,41 @@ extern "C" int gemm_rs_bwd_run(gemm_rs_bwd_t h, const void* dY, const void* W, c
     ok = ok && make_map(&p.dy_k, dY, h->N, h->M, 1, kBK, 128) && make_map(&p.w_k, W, h->N, h->Kr, kWorld, kBK, 128) &&
          make_map(&p.out_da, dA, h->Kr, h->M, kWorld, 64, 32);
   if (dw) {
-    ok = ok && make_map(&p.a_mn, workspace, h->Kr, h->M, kWorld, 64, kBK, act8_pitch(h->Kr)) &&
+    ok = ok && make_map(&p.a_mn, restored, h->Kr, h->M, kWorld, 64, kBK, act8_pitch(h->Kr)) &&
          make_map(&p.dy_mn, dY, h->N, h->M, 1, 64, kBK) && make_map(&p.out_dw, dW, h->N, h->Kr, kWorld, 64, 32);
     // A small checkpoint is restored beside the first dA tiles; a large one is
     // faster with the whole GPU to itself.
     p.restored_before = da && h->M * h->K <= kRestoreBeside;
-    const int rc = act8_restore_padded(h->M, h->K, codes, scales, workspace, p.restored_before, stream);
+    const int rc = act8_restore_padded(h->M, h->K, codes, scales, restored, p.restored_before, stream);
     if (rc) return rc;
   }
   if (!ok) return GEMM_RS_ERR_CUDA;
   p.s = schedule_of(da ? product_of(h->M, h->Kr, h->N) : none, dw ? product_of(h->Kr, h->N, h->M) : none,
                     h->max_pairs);
-  return launch_overlapped(backward_kernel, dim3(2u * (unsigned)p.s.pairs), 32 * kWarps, kSmemAlloc, st, p);
+  const int ctas = 2 * p.s.pairs;
+  const int rc = launch_overlapped(backward_kernel, dim3((unsigned)ctas), 32 * kWarps, kSmemAlloc, st, p);
+  if (rc) return rc;
+  h->last_ws = workspace;
+  h->last_ctas = ctas;
+  return GEMM_RS_OK;
 }
 
 extern "C" int gemm_rs_bwd_status(gemm_rs_bwd_t h, void* stream) {
   if (!h) return GEMM_RS_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  uint32_t word = 0;
+  uint32_t words[kStatusWords];
   cudaError_t e = cudaStreamSynchronize(st);
   if (e == cudaSuccess && h->last_ws) {
-    uint8_t* error = static_cast<uint8_t*>(h->last_ws) + h->a_bytes;
-    e = cudaMemcpyAsync(&word, error, 4, cudaMemcpyDeviceToHost, st);
+    e = cudaMemcpyAsync(words, h->last_ws, h->last_ctas * sizeof(uint32_t), cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess && word) {
-      e = cudaMemsetAsync(error, 0, 4, st);  // the next run starts clean
-      if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    }
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
     return GEMM_RS_ERR_CUDA;
   }
-  return word ? GEMM_RS_ERR_TIMEOUT : GEMM_RS_OK;
+  for (int i = 0; h->last_ws && i < h->last_ctas; ++i)
+    if (words[i]) return GEMM_RS_ERR_TIMEOUT;
+  return GEMM_RS_OK;
 }
 
 extern "C" int gemm_rs_bwd_destroy(gemm_rs_bwd_t h) {

@@ -223,6 +223,63 @@ def test_empty_contractions():
 
 
 @pytest.mark.gpu
+def test_status_is_the_runs_whatever_becomes_of_its_workspace():
+    M, N, K = 72, 136, 576
+    A, W, dY = (t.cuda() for t in problem(M, N, K, seed=21))
+    plan, ck = act8.BackwardPlan(M, N, K), act8.save(A)
+    dA, dW = torch.empty_like(A), torch.empty_like(W)
+
+    def filled():
+        return plan.new_workspace().fill_(0xFF)
+
+    for outs in ((dA, dW), (dA, None), (None, dW)):
+        for _ in range(3):  # a workspace of the call alone; its place, if it is free, holds something else by now
+            plan.run(dY, W, ck, *outs, filled())
+            others = [filled() for _ in range(4)]
+            assert plan.status() == G.GEMM_RS_OK
+            assert all((t == 0xFF).all() for t in others)
+            del others
+    plan.run(dY, W, ck, None, None, filled())  # nothing to compute
+    others = [filled() for _ in range(4)]
+    assert plan.status() == G.GEMM_RS_OK
+    assert all((t == 0xFF).all() for t in others)
+
+
+@pytest.mark.gpu
+def test_plans_share_a_workspace():
+    """The larger one's restored activations do not look like the smaller one's failure."""
+    sizes = [(8, 264, 512), (392, 776, 1600), (136, 392, 2624)]
+    inputs = [problem(*s, seed=31) for s in sizes]
+    plans = [act8.BackwardPlan(*s) for s in sizes]
+    ws = max((p.new_workspace() for p in plans), key=lambda t: t.numel()).fill_(0xFF)
+    for _ in range(2):
+        for size, (A, W, dY), plan in zip(sizes, inputs, plans):
+            dA, dW = run(*size, A, W, dY, plan=plan, ws=ws)
+            assert all(p.status() == G.GEMM_RS_OK for p in plans[:plans.index(plan) + 1])
+            assert_products(dA, dW, dY, W, checkpoint_values(f64(A)))
+
+
+@pytest.mark.gpu
+def test_a_plan_first_seen_by_a_graph():
+    M, N, K = 72, 136, 576
+    A, W, dY = (t.cuda() for t in problem(M, N, K, seed=22))
+    plan, ck = act8.BackwardPlan(M, N, K), act8.save(A)
+    ws, dA, dW = plan.new_workspace().fill_(0xFF), torch.empty_like(A), torch.empty_like(W)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.run(dY, W, ck, dA, dW, ws)
+    plan.run(dY, W, ck, dA, dW, ws)
+    assert plan.status() == G.GEMM_RS_OK
+    want = dA.clone(), dW.clone()
+    ws.fill_(0xFF)
+    dA.zero_()
+    dW.zero_()
+    graph.replay()
+    assert plan.status() == G.GEMM_RS_OK
+    assert torch.equal(dA, want[0]) and torch.equal(dW, want[1])
+
+
+@pytest.mark.gpu
 def test_tensor_refusals():
     A, W, dY = (t.cuda() for t in problem(16, 64, 512, seed=1))
     with pytest.raises(TypeError):
