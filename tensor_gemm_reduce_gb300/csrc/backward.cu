@@ -18,9 +18,10 @@
 // library product sustains and 0.86 of its burst; 512 x 8192 x 28672 334 to 340 us,
 // 1.42 PFLOP/s (its dW tiles contract over 8 steps, so what a tile costs besides,
 // 500 to 1000 cycles, and 1 GB of operands and outputs weigh more).
-// Every wait is bounded; on expiry the kernel lets its copies land, frees TMEM and
-// returns.  Each CTA says at its end, in a word of its own, whether it gave up, so
-// nothing has to be cleared before a run, whatever the workspace held.
+// Every wait is bounded; on expiry both CTAs of the pair stop, leave their copies and
+// MMAs the time to end, free TMEM and return.  Each CTA says at its end, in a word of
+// its own, whether it gave up, so nothing has to be cleared before a run, whatever the
+// workspace held.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -53,6 +54,9 @@ static_assert(kSmemAlloc <= 232448, "shared memory per CTA");
 // 12928 16.0 -> 17.0, 1000 x 1032 x 6400 35.8 -> 37.1, the largest no difference).
 constexpr int64_t kRestoreBeside = 2 << 20;
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+// What is in flight when a CTA has nothing more to issue ends within microseconds.
+constexpr uint64_t kDrainNs = 100000000ull;   // bound of the waits for it, whatever the caller's limit
+constexpr uint64_t kSettleNs = 10000000ull;   // time that a pair leaves it after giving up
 // The workspace: a status word for each CTA, then the restored activations.  The words
 // come first so that plans of any sizes which share a workspace agree on the place.
 constexpr int kStatusWords = 256;
@@ -140,6 +144,21 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t
   }
 }
 
+// A wait ran out: both CTAs of the pair stop at their next wait that does not succeed.
+__device__ __forceinline__ void give_up(uint32_t abort_addr) {
+#pragma unroll
+  for (uint32_t cta = 0; cta < 2; ++cta)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(abort_addr, cta)), "r"(1) : "memory");
+}
+
+// Time for the copies and MMAs of a pair that gave up.  Waiting for their barriers does
+// not do: a stage that one of the pair's four loaders never filled never completes, and
+// the others' bytes for it may still be on their way.
+__device__ __noinline__ void settle() {
+  const uint64_t t0 = globaltimer_ns();
+  for (int i = 0; i < (1 << 20) && globaltimer_ns() - t0 < kSettleNs; ++i) __nanosleep(1000);
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
     backward_kernel(const __grid_constant__ BwdParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -156,6 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
   const uint32_t bar_drain = bar_acc_empty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSmemMisc);
   volatile uint32_t* cta_abort = reinterpret_cast<volatile uint32_t*>(smem + kSmemMisc + 4);
+  const uint32_t abort_addr = sbase + kSmemMisc + 4;
   const uint64_t limit = p.timeout_ns;
 
   if (threadIdx.x == 0) {
@@ -208,7 +228,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
         const int x0 = (is_a ? t.mt : t.nt) * kTile + cta * 128;
         for (int kb = 0; kb < kb_count; ++kb) {
           if (!wait_bar(bar_empty + 8 * stage, phase ^ 1u, limit, cta_abort)) {
-            *cta_abort = 1;
+            give_up(abort_addr);
             ok = false;
             break;
           }
@@ -234,11 +254,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
           }
         }
       }
+      // the grid does not end before the restoration (a pair without dW tiles has not waited)
+      if (is_a && !waited) griddep_wait();
       // every copy lands before the CTA can exit (the first CTA's barriers
-      // count both CTAs' bytes)
+      // count both CTAs' bytes; a pair that gave up waits in settle() below)
       if (cta == 0)
         for (int s = 0; s < kStages; ++s)
-          if (issued & (1u << s)) wait_bar(bar_full + 8 * s, (issued_par >> s) & 1u, limit, cta_abort);
+          if ((issued & (1u << s)) && !wait_bar(bar_full + 8 * s, (issued_par >> s) & 1u, kDrainNs, cta_abort))
+            give_up(abort_addr);
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
@@ -255,7 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
       bool ok = true;
       while (ok && walk.next(p.s, &t)) {
         if (!wait_bar(bar_acc_empty + 8 * acc, acc_phase ^ 1u, limit, cta_abort, true)) {
-          *cta_abort = 1;
+          give_up(abort_addr);
           break;
         }
         tc_fence_after();
@@ -266,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
         const int kb_count = t.is_dw ? p.s.dw.kb : p.s.da.kb;
         for (int kb = 0; kb < kb_count; ++kb) {
           if (!wait_bar(bar_full + 8 * stage, phase, limit, cta_abort)) {
-            *cta_abort = 1;
+            give_up(abort_addr);
             ok = false;
             break;
           }
@@ -289,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
         if (acc == 0) acc_phase ^= 1u;
       }
       mma_commit<2>(bar_drain);  // every MMA completes before TMEM is released
-      wait_bar(bar_drain, 0, limit, cta_abort);
+      if (!wait_bar(bar_drain, 0, kDrainNs, cta_abort)) give_up(abort_addr);
     }
   } else {
     // ---------------------------------------------------------------- epilogue
@@ -304,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
       if (lane == 0) got = wait_bar(bar_acc_full + 8 * acc, acc_phase, limit, cta_abort) ? 1 : 0;
       got = __shfl_sync(0xffffffffu, got, 0);
       if (!got) {
-        if (lane == 0) *cta_abort = 1;
+        if (lane == 0) give_up(abort_addr);
         break;
       }
       tc_fence_after();
@@ -365,8 +388,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * kWarps, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) p.status[blockIdx.x] = *cta_abort;
-  cluster_sync();  // no MMA or remote arrival targets this CTA any more
+  cluster_sync();  // neither CTA issues anything more, and what it issued has ended
+  const uint32_t gave_up = *cta_abort;  // the same in both CTAs
+  if (gave_up) settle();                // or has now
+  if (threadIdx.x == 0) p.status[blockIdx.x] = gave_up;
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<2>(tmem_base, 512);

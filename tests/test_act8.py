@@ -280,6 +280,30 @@ def test_a_plan_first_seen_by_a_graph():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(8, 1 << 17, 64), (264, 1 << 16, 2112)])
+@pytest.mark.parametrize("da,dw", [(True, True), (True, False)])
+def test_a_wait_that_runs_out_is_reported(M, N, K, da, dw):
+    """A dA tile's sums take 1024 steps or more, 0.3 ms; the warps that wait for them may wait 1 us.
+    The run ends, says so, and leaves nothing behind: the next runs give what the one before gave."""
+    A, W, dY = (torch.randn(s, device="cuda", generator=torch.Generator("cuda").manual_seed(6)).to(torch.bfloat16)
+                for s in ((8, M, K // 8), (8, K // 8, N), (M, N)))
+    ck = act8.save(A)
+    good, bad = act8.BackwardPlan(M, N, K), act8.BackwardPlan(M, N, K, timeout_ns=1000)
+    ws = good.new_workspace()
+    outs = torch.empty_like(A) if da else None, torch.empty_like(W) if dw else None
+    good.run(dY, W, ck, *outs, ws)
+    assert good.status() == G.GEMM_RS_OK
+    want = [None if t is None else t.clone() for t in outs]
+    for _ in range(3):
+        bad.run(dY, W, ck, *outs, ws)
+        assert bad.status() == bad.status() == G.GEMM_RS_ERR_TIMEOUT
+        good.run(dY, W, ck, *outs, ws)
+        assert good.status() == G.GEMM_RS_OK
+        for t, w in zip(outs, want):
+            assert t is None or torch.equal(t, w)
+
+
+@pytest.mark.gpu
 def test_tensor_refusals():
     A, W, dY = (t.cuda() for t in problem(16, 64, 512, seed=1))
     with pytest.raises(TypeError):
