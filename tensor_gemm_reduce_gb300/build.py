@@ -1,5 +1,5 @@
 """Build the CUDA library in-tree: tensor_gemm_reduce_gb300/lib/libgemm_rs.so,
-and the Python entry of its operators beside it (_ops.so).
+and the Python entry of its operators beside it (_ops_<hash>.so).
 
 Sources compile for sm_103a (tcgen05 / TMA need the arch-specific target) side
 by side, one nvcc for each, and are linked into one library.  The library links the CUDA runtime statically and resolves the one driver call
@@ -8,6 +8,9 @@ dependency on libcuda.
 """
 from __future__ import annotations
 
+import contextlib
+import glob
+import hashlib
 import os
 import shutil
 import subprocess
@@ -25,8 +28,8 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("kernels.cuh", "ptx.cuh", "sch
                                                   "ops_common.cuh", "act8.cuh")] + [
     os.path.join(ROOT, "include", f) for f in ("gemm_rs.h", "gemm_rs_ops.h")]
 
-BINDING = os.path.join(LIBDIR, "_ops.so")
 BINDING_SOURCE = os.path.join(CSRC, "ops_binding.cpp")
+BINDING_HEADERS = [os.path.join(ROOT, "include", f) for f in ("gemm_rs.h", "gemm_rs_ops.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -78,16 +81,27 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=None) 
     return LIB
 
 
+def binding_path() -> str:
+    """Where the binding lies that was compiled from these sources for this torch and Python.  One
+    of another interface or another torch has another name, so it is never loaded in its place."""
+    import torch
+    h = hashlib.sha256(f"{torch.__version__} {sys.version}".encode())
+    for path in [BINDING_SOURCE] + BINDING_HEADERS:
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return os.path.join(LIBDIR, f"_ops_{h.hexdigest()[:12]}.so")
+
+
 def build_binding(force: bool = False) -> str:
     """Compile csrc/ops_binding.cpp against torch and the library; return its path."""
+    binding = binding_path()
+    if not force and os.path.exists(binding):
+        return binding
     lib = build_library()
-    headers = [os.path.join(ROOT, "include", f) for f in ("gemm_rs.h", "gemm_rs_ops.h")]
-    if not force and not _stale(BINDING, [BINDING_SOURCE] + headers):
-        return BINDING
     import torch
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = binding + f".tmp{os.getpid()}"
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-o", tmp, BINDING_SOURCE,
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
     for inc in (sysconfig.get_paths()["include"], os.path.join(home, "include"),
@@ -98,8 +112,11 @@ def build_binding(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    for old in glob.glob(os.path.join(LIBDIR, "_ops*.so")):
+        with contextlib.suppress(FileNotFoundError):  # another process built it too
+            os.remove(old)
+    os.replace(tmp, binding)
+    return binding
 
 
 if __name__ == "__main__":

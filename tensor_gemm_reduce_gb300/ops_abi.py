@@ -72,11 +72,11 @@ _OPS = None
 
 
 def ops():
-    """The compiled entry of the operators (built first if it is missing)."""
+    """The compiled entry of the operators (built first if there is none of these sources)."""
     global _OPS
     if _OPS is None:
         lib()
-        path = _build.BINDING if os.path.exists(_build.BINDING) else _build.build_binding()
+        path = _build.build_binding()
         loader = importlib.machinery.ExtensionFileLoader("_ops", path)
         spec = importlib.util.spec_from_file_location("_ops", path, loader=loader)
         module = importlib.util.module_from_spec(spec)
