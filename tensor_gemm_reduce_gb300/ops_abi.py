@@ -108,14 +108,16 @@ def allocating_for(stream):
     return _AS_IT_IS if stream is None else torch.cuda.stream(stream)
 
 
-def pointer(t, shape, dtype, name: str) -> int:
-    """Address of a contiguous CUDA tensor of this shape and dtype."""
+def pointer(t, shape, dtype, name: str, device=None) -> int:
+    """Address of a contiguous CUDA tensor of this shape and dtype (on `device`)."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
     return t.data_ptr()
 
 

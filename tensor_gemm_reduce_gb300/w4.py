@@ -62,8 +62,8 @@ def pack(codes, scales, zeros=None, group: int = 128, stream=None) -> Weight:
     _, Kr, N = codes.shape
     per_group = torch.Size((_a.WORLD, _groups(Kr, group), N))
     c = _a.pointer(codes, codes.shape, _U8, "codes")
-    s = _a.pointer(scales, per_group, _BF16, "scales")
-    z = None if zeros is None else _a.pointer(zeros, per_group, _U8, "zeros")
+    s = _a.pointer(scales, per_group, _BF16, "scales", codes.device)
+    z = None if zeros is None else _a.pointer(zeros, per_group, _U8, "zeros", codes.device)
     with _a.allocating_for(stream):
         weight = Weight(N, Kr * _a.WORLD, group, zeros is not None, codes.device)
     _a.check(_a.lib().gemm_rs_w4_pack(N, weight.K, group, c, s, z, weight.data.data_ptr(),

@@ -9,6 +9,7 @@ the absolute terms.  The result is rounded once: half a bf16 step is at most
 2**-8 of the value.
 """
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -187,6 +188,19 @@ def test_other_refusals():
     assert lib.gemm_rs_w4_quantize(64, 512, 128, None, None, None, None) == G.GEMM_RS_ERR_INVALID_ARG
     with pytest.raises(ValueError):
         w4.pack(torch.zeros(8, 64, 8, dtype=torch.uint8), torch.zeros(8, 1, 8, dtype=torch.bfloat16), group=64)
+
+
+@pytest.mark.parametrize("other", ["scales", "zeros"])
+def test_pack_takes_tensors_of_one_device(other):
+    """Tensors of two devices, as far as their attributes go."""
+    def tensor(shape, dtype, device):
+        return types.SimpleNamespace(shape=torch.Size(shape), dtype=dtype, device=torch.device(device), is_cuda=True,
+                                     dim=lambda: len(shape), is_contiguous=lambda: True, data_ptr=lambda: 16)
+
+    at = {"codes": "cuda:0", "scales": "cuda:0", "zeros": "cuda:0", other: "cuda:1"}
+    with pytest.raises(ValueError, match=f"{other} is on cuda:1"):
+        w4.pack(tensor((8, 64, 8), torch.uint8, at["codes"]), tensor((8, 1, 8), torch.bfloat16, at["scales"]),
+                tensor((8, 1, 8), torch.uint8, at["zeros"]), group=64)
 
 
 def test_packed_size_is_near_half_a_byte_a_weight():
