@@ -163,6 +163,19 @@ def test_backward_matches_the_formula(M, D, gate_rows):
         assert a is None or torch.equal(a, b)  # the sums have a fixed order
 
 
+# three vectors a thread (4104 to 5632 and 8200 to 12288 columns) with a gate row for each row, where the weights lie
+# in shared memory and the ring has five arrays, and with one or some; four vectors a thread with each
+LONG = [(40, 4104, 40), (161, 4608, 161), (9, 5632, 9), (305, 8200, 305), (6, 12288, 6), (154, 12288, 154),
+        (306, 5632, 3), (160, 9216, 10), (155, 8200, 1), (4, 12296, 4), (160, 12296, 20), (153, 16384, 1)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,D,gate_rows", LONG)
+def test_long_rows(M, D, gate_rows):
+    test_forward_matches_the_formula(M, D, gate_rows, 0.6)
+    test_backward_matches_the_formula(M, D, gate_rows)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,D,gate_rows", [(6, 32, 0), (6, 32, 1), (6, 40, 3), (160, 16, 4), (5, 24, 5)])
 def test_backward_matches_differences(M, D, gate_rows):

@@ -79,6 +79,20 @@ def test_matvec_matches_the_formula(M, N, K, group, zeros):
         assert torch.equal(w4.matvec(dx, weight), out)
 
 
+# many columns: 4 warps of columns a CTA (up to 16 tokens from 3969 columns on, above from 1985), 8 (above 16 tokens,
+# from 3969), with parts of the inner dimension beside them (4104 columns) or not, ragged last columns, and more
+# clusters than run at once (from 12288 columns on), where the first weights are not asked for early
+WIDE = [(1, 8192, 1024), (3, 4104, 8256), (16, 6152, 1600), (9, 4000, 576), (24, 2568, 1600), (17, 3960, 2112),
+        (32, 4104, 2112), (24, 6152, 1088), (4, 12288, 576), (1, 16392, 512), (12, 12296, 1024), (32, 12288, 576)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", WIDE)
+@pytest.mark.parametrize("group,zeros", [(128, False), (64, True), (32, True)])
+def test_many_columns(M, N, K, group, zeros):
+    test_matvec_matches_the_formula(M, N, K, group, zeros)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 2, 4, 7, 8, 10, 15, 16, 23, 25, 31, 32])
 def test_every_token_count_gives_the_same_rows(M):
