@@ -96,8 +96,9 @@ int gemm_rs_act8_restore(int64_t M, int64_t K, const void* codes, const void* sc
  * it is not needed (W, or codes and scales, may then be NULL too). */
 typedef struct gemm_rs_bwd_plan_s* gemm_rs_bwd_t;
 
-/* timeout_ns: bound on every device-side wait; 0 = 2 s.  Shapes are checked
- * before any CUDA call.  N % 8 == 0, the others as above. */
+/* timeout_ns: bound on every device-side wait; 0 = 2 s (a run that gives up takes
+ * about 10 ms more to end).  Shapes are checked before any CUDA call.  N % 8 == 0,
+ * the others as above.  The plan is for the device that is current here. */
 int gemm_rs_bwd_create(int64_t M, int64_t N, int64_t K, uint64_t timeout_ns, gemm_rs_bwd_t* plan,
                        size_t* workspace_bytes);
 /* The workspace needs no initialisation, and plans that follow one another on a

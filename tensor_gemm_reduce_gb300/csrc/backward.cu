@@ -15,7 +15,7 @@
 // Bound by the tensor cores and, in a row of launches, by the card's power: 2048 x
 // 8192 x 8192 (550 GFLOP) takes 276 us alone at the full clock (tensor pipe active
 // 94%) and 330 us repeated, restore included: 1.65 PFLOP/s, 0.98 of what a plain
-// library product sustains and 0.86 of its burst; 512 x 8192 x 28672 334 to 340 us,
+// library product sustains and 0.86 of its burst; 512 x 8192 x 28672 338 us,
 // 1.42 PFLOP/s (its dW tiles contract over 8 steps, so what a tile costs besides,
 // 500 to 1000 cycles, and 1 GB of operands and outputs weigh more).
 // Every wait is bounded; on expiry both CTAs of the pair stop, leave their copies and

@@ -4,10 +4,10 @@
 //
 // Both passes read each row once and are bound by HBM: 8 bytes an element forward,
 // 12 backward (14 and 16 with a gate value for each).  Measured on a GB300, whose
-// copies reach 6.79 TB/s: forward 2048 x 8192 with 4 gate rows 25.3 us (5.3 TB/s),
-// 8192 x 8192 84.9 us (6.3 TB/s), one row 3.4 us; backward 8192 x 8192 with the join
+// copies reach 6.79 TB/s: forward 2048 x 8192 with 4 gate rows 25.6 us (5.2 TB/s),
+// 8192 x 8192 85.1 us (6.3 TB/s), one row 3.5 us; backward 8192 x 8192 with the join
 // of the sums over rows 125 us (6.4 TB/s), 1003 x 6152 with a gate value for each
-// element 25.6 us (3.9 TB/s: 7 rows a block, of which the first and the last run
+// element 25.5 us (3.9 TB/s: 7 rows a block, of which the first and the last run
 // beside nothing, and 3.5 us of join).
 #include <cmath>
 

@@ -24,10 +24,13 @@
 // the layer's reduce-scatter, inside one cluster.  Inside a CTA the warps take
 // columns, and where there are few columns also parts of the inner dimension.
 //
-// Measured, us: one token, 8192 columns, K = 28672 (121 MB) 23.8, 5.1 TB/s, 0.75 of
-// a copy's rate; K = 8192 9.5, where the clusters' start and joins count as much as
-// the weights.  16 tokens, 6144 columns, K = 16384 19.1; 32 tokens 32: 12 to 16
-// warps an SM hide too little of the latency of unpacking, MMA and scaling.
+// Measured, us, calls in a row over weights of 12 layers in turn, which L2 does not
+// hold: one token, 8192 columns, K = 28672 with zero points (122 MB) 24.8, 4.9 TB/s,
+// 0.72 of a copy's rate; K = 8192 10.0, where the clusters' start and joins count as
+// much as the weights.  16 tokens, 6144 columns, K = 16384, groups of 64 19.3; 32
+// tokens 37.6, in groups of 128 32.7: 12 to 16 warps an SM hide too little of the
+// latency of unpacking, MMA and scaling.  (Three layers in turn, of which L2 holds much:
+// 24.3, 8.6, 18.4, 37.2 and 32.3.)
 #include "ops_common.cuh"
 
 using namespace grs;

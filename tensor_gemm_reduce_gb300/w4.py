@@ -72,13 +72,15 @@ def pack(codes, scales, zeros=None, group: int = 128, stream=None) -> Weight:
 
 
 def new_workspace(weight: Weight):
-    """Workspace of matvec(): empty, its sums meet in the SMs' shared memory.  It is
-    there so that callers can treat this layer like the library's others."""
+    """A placeholder for matvec()'s `workspace`: an empty tensor.  The sums meet in the SMs'
+    shared memory; the two are there so that callers can treat this layer like the library's
+    others."""
     return torch.empty(0, dtype=_U8, device=weight.data.device)
 
 
 def matvec(x, weight: Weight, out=None, workspace=None, stream=None):
-    """out [M][N] = the layer's output for x [8][M][K/8], M at most 32."""
+    """out [M][N] = the layer's output for x [8][M][K/8], M at most 32.  `workspace` is a
+    placeholder: it is not used."""
     if out is None:
         if x.dim() != 3:
             raise ValueError(f"x must have shape [{_a.WORLD}][M][K/{_a.WORLD}], got {tuple(x.shape)}")
