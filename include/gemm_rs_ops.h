@@ -102,8 +102,8 @@ typedef struct gemm_rs_bwd_plan_s* gemm_rs_bwd_t;
 int gemm_rs_bwd_create(int64_t M, int64_t N, int64_t K, uint64_t timeout_ns, gemm_rs_bwd_t* plan,
                        size_t* workspace_bytes);
 /* The workspace needs no initialisation, and plans that follow one another on a
- * stream may share one.  It stays allocated until the run's status has been
- * asked for, or never is.  A plan serves one stream at a time. */
+ * stream may share one.  gemm_rs_bwd_status reads it, so it stays allocated until
+ * the last call of that for this run.  A plan serves one stream at a time. */
 int gemm_rs_bwd_run(gemm_rs_bwd_t plan, const void* dY, const void* W, const void* codes,
                     const void* scales, void* dA, void* dW, void* workspace, void* stream);
 /* Status of the last run in the plan's last workspace, which it reads and does not
