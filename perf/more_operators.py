@@ -3,7 +3,7 @@ one weight and for the weights of several experts, as they are measured.
 
 route: scores, choice and weights of each token's experts, the order of the
 token-expert pairs by expert, and the gradient of the scores; layer: out =
-sum_r A_r W_r in e4m3 with a power of two for each block of 128, forward and backward;
+sum_r A_r W_r in e4m3 with a scale for each block of 128, forward and backward;
 experts: the same product for each expert's tokens, weighted and summed for each
 token.  M tokens (T where they are routed), N output columns, K inner dimension
 over 8 virtual ranks, E experts, k of them for a token.
@@ -17,7 +17,7 @@ own = False
 WORLD = 8
 BLOCK = 128
 LARGEST = 448.0  # of e4m3
-LEAST = -126  # exponent of a block's scale
+SMALLEST = 2.0 ** -100  # a block's largest magnitude counts as at least this
 SCALE = 1.5  # of the routed weights where they are not renormalised
 
 
@@ -176,14 +176,12 @@ def prepare(case, seed):
 
 def _codes(x, rows, cols):
     """e4m3 codes of x's last two dimensions in blocks of rows x cols, padded to whole
-    blocks [..., R, rows, C, cols], and the blocks' scales [..., R, 1, C, 1]: the least
-    power of two whose LARGEST-fold holds the block."""
+    blocks [..., R, rows, C, cols], and the blocks' scales [..., R, 1, C, 1]."""
     r, c = x.shape[-2:]
     x = torch.nn.functional.pad(x, (0, -c % cols, 0, -r % rows))
     x = x.unflatten(-1, (-1, cols)).unflatten(-3, (-1, rows)).float()
-    m, ex = torch.frexp(x.abs().amax((-3, -1), keepdim=True))  # LARGEST is 0.875 * 2^9
-    e = (ex - 9 + (m > 0.875)).clamp(min=LEAST)
-    return torch.ldexp(x, -e).to(torch.float8_e4m3fn), torch.ldexp(torch.ones_like(m), e)
+    scale = x.abs().amax((-3, -1), keepdim=True).clamp(min=SMALLEST) * (1 / LARGEST)
+    return (x * scale.reciprocal()).to(torch.float8_e4m3fn), scale
 
 
 def _values(codes, scales, shape):
@@ -362,18 +360,20 @@ def work(case):
 
 
 def _exact_rounded(x, rows, cols):
-    """The values that x has in blocks of rows x cols: the nearest of e4m3's for x / scale, ties
-    to the even one."""
+    """The values that x has in blocks of rows x cols: a scale of 32 bits, the least of e4m3's
+    magnitudes' distances from x / scale, ties to the even one."""
     r, c = x.shape[-2:]
     R, C = -(-r // rows), -(-c // cols)
     full = torch.zeros(*x.shape[:-2], R * rows, C * cols, dtype=torch.float64, device=x.device)
     full[..., :r, :c] = x
-    top = full.abs().unfold(-2, rows, rows).unfold(-2, cols, cols).amax((-2, -1))
-    scale = torch.pow(2.0, torch.ceil(torch.log2(top / LARGEST)).clamp(min=LEAST))
-    scale = scale.repeat_interleave(rows, -2).repeat_interleave(cols, -1)
-    v = full / scale
+    top = full.abs().unfold(-2, rows, rows).unfold(-2, cols, cols).amax((-2, -1)).clamp(min=SMALLEST)
+    scale = top.float() * torch.tensor(1 / LARGEST, dtype=torch.float32, device=x.device)
+    inverse = (1 / scale).double().repeat_interleave(rows, -2).repeat_interleave(cols, -1)
+    scale = scale.double().repeat_interleave(rows, -2).repeat_interleave(cols, -1)
+    v = (full * inverse).float().double()
     step = torch.pow(2.0, (torch.frexp(v).exponent - 1).clamp(min=-6).double() - 3)
-    return (torch.round(v / step) * step * scale)[..., :r, :c]
+    v = (torch.round(v / step) * step).clamp(-LARGEST, LARGEST)
+    return (v * scale)[..., :r, :c]
 
 
 def _exact_route(s):
