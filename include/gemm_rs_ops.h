@@ -7,8 +7,8 @@
  *   act8   the layer's input kept in 8 bits between the forward and the
  *          backward pass, and the layer's backward pass from it (gemm_rs_bwd_*)
  *   w4     the layer for 1 to 32 tokens, with 4-bit weights and group scales
- *   fp8    the layer in 8-bit floating point with a power of two for each block of
- *          128, forward and backward
+ *   fp8    the layer in 8-bit floating point with a scale for each block of 128,
+ *          forward and backward
  *   moe    routing to experts, and their layer in fp8 with a weight for each
  *          token and expert, forward and backward
  *
@@ -146,24 +146,35 @@ int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int has_zeros, co
 
 /* -------------------------------------------------------------------- fp8
  * The row-parallel layer in e4m3 (4 bits of exponent, 3 of mantissa, largest
- * 448) with a power of two for each block of 128: 2^e with the least e >= -126
- * such that the block's largest magnitude is at most 448 * 2^e; a code is the
- * element over 2^e, rounded to nearest even.  A block with an infinity or a NaN
- * has the scale NaN and NaN codes, and so makes NaN of every output that it takes
- * part in.  In the products
+ * 448) with a scale for each block of 128.  A block's scale is
+ * max(largest magnitude, 2^-100) * fp32(1/448), rounded to fp32; a code is the
+ * element times the scale's fp32 reciprocal, rounded to fp32, then to e4m3, to
+ * nearest even.  A block with an infinity or a NaN has the scale NaN and NaN codes,
+ * and so makes NaN of every output that it takes part in.  In the products
  *
  *   out    = sum_r A_r W_r     A in 1 x 128 blocks along K/8, W in 128 x 128
  *   dA_r   = dY W_r^T          dY in 1 x 128 blocks along N, W as above
  *   dW_r   = A_r^T dY          A and dY in blocks of 128 tokens for each column
  *
- * scaled codes are multiplied and summed on the tensor cores in fp32, and outputs
- * rounded to bf16 once.  The same call gives the same bits; with other rows beside it, or for dA
- * without dW, a sum may run in another order.
+ * the codes of a step of 128 inner elements are multiplied and summed on the
+ * tensor cores in fp32, scaled by the product of the two scales, and added up
+ * in fp32; outputs are rounded to bf16 once.  The same call gives the same bits; with
+ * other rows beside it, or for dA without dW, a sum may run in another order.
  *
  * Weights: codes [experts][8][ceil(N/128)][K/8][128] e4m3 (128 columns of W at a
  * time; zero behind the last column) and scales [experts][8][ceil(K/8/128)]
- * [ceil(N/128)] e8m0 (bytes: e + 127, 255 is NaN).  Codes and scales made
- * elsewhere in this layout serve as well.  experts is 1 for the layer itself.
+ * [ceil(N/128)] fp32.  Codes and scales made elsewhere in this layout serve as
+ * well.  experts is 1 for the layer itself.
+ *
+ * The entries whose names end in _e8m0 are the same in a form that large products
+ * take half the time in, for some accuracy: every block's scale, of weights, inputs and
+ * gradients alike, is a power of two, 2^e with the least e >= -126 such that the
+ * block's largest magnitude is at most 448 * 2^e; codes are the elements over 2^e,
+ * and the tensor cores apply the scales, so that the whole contraction is summed in
+ * their fp32 (which may truncate where it aligns addends).  The weights' scales are
+ * bytes, e + 127, 255 for NaN.  Inputs with one entry in 20 eight times as large are rounded by
+ * 2.7% of their norm in this form, and by 2.1% in the other.  A checkpoint serves the form that wrote it.
+ *
  * N % 8 == 0, K % 64 == 0, any M; 0 allowed. */
 #define GEMM_RS_FP8_MAX_EXPERTS 256
 int gemm_rs_fp8_weight_bytes(int64_t experts, int64_t N, int64_t K, size_t* code_bytes,
@@ -171,11 +182,15 @@ int gemm_rs_fp8_weight_bytes(int64_t experts, int64_t N, int64_t K, size_t* code
 /* Codes and scales of W [experts][8][K/8][N] bf16. */
 int gemm_rs_fp8_quantize(int64_t experts, int64_t N, int64_t K, const void* W, void* codes,
                          void* scales, void* stream);
+int gemm_rs_fp8_weight_bytes_e8m0(int64_t experts, int64_t N, int64_t K, size_t* code_bytes,
+                                  size_t* scale_bytes); /* host only */
+int gemm_rs_fp8_quantize_e8m0(int64_t experts, int64_t N, int64_t K, const void* W, void* codes,
+                              void* scales, void* stream);
 /* What the backward pass keeps of A: its codes in blocks of 128 tokens and their
- * scales, contents private to this library. */
+ * scales, contents private to this library.  Either form's. */
 int gemm_rs_fp8_checkpoint_bytes(int64_t M, int64_t K, size_t* code_bytes,
                                  size_t* scale_bytes); /* host only */
-/* Bytes of workspace of either pass (host only).  It needs no initialisation. */
+/* Bytes of workspace of either pass in either form (host only).  It needs no initialisation. */
 int gemm_rs_fp8_workspace(int64_t M, int64_t N, int64_t K, size_t* bytes);
 /* A [8][M][K/8], out [M][N] bf16; codes and scales of the weight.  ck_codes and
  * ck_scales (both or neither) take what the backward pass needs. */
@@ -187,6 +202,12 @@ int gemm_rs_fp8_forward(int64_t M, int64_t N, int64_t K, const void* A, const vo
 int gemm_rs_fp8_backward(int64_t M, int64_t N, int64_t K, const void* dY, const void* codes,
                          const void* scales, const void* ck_codes, const void* ck_scales,
                          void* dA, void* dW, void* workspace, void* stream);
+int gemm_rs_fp8_forward_e8m0(int64_t M, int64_t N, int64_t K, const void* A, const void* codes,
+                             const void* scales, void* ck_codes, void* ck_scales, void* out,
+                             void* workspace, void* stream);
+int gemm_rs_fp8_backward_e8m0(int64_t M, int64_t N, int64_t K, const void* dY, const void* codes,
+                              const void* scales, const void* ck_codes, const void* ck_scales,
+                              void* dA, void* dW, void* workspace, void* stream);
 /* Device-side waits are bounded (2 s).  The status of the last call with this
  * workspace: synchronises `stream`; GEMM_RS_OK, GEMM_RS_ERR_TIMEOUT (a wait gave
  * up, the outputs are incomplete) or GEMM_RS_ERR_CUDA. */
@@ -276,6 +297,16 @@ int gemm_rs_moe_backward(const gemm_rs_moe_desc* d, const void* dout, const void
                          const void* pairs, const void* offsets, const void* ck_codes,
                          const void* ck_scales, const void* ck_y, void* dA, void* dW,
                          void* dweights, void* workspace, void* stream);
+/* With scales that are powers of two (see fp8). */
+int gemm_rs_moe_forward_e8m0(const gemm_rs_moe_desc* d, const void* A, const void* codes,
+                             const void* scales, const void* weights, const void* rows,
+                             const void* offsets, void* ck_codes, void* ck_scales, void* ck_y,
+                             void* out, void* workspace, void* stream);
+int gemm_rs_moe_backward_e8m0(const gemm_rs_moe_desc* d, const void* dout, const void* codes,
+                              const void* scales, const void* weights, const void* rows,
+                              const void* pairs, const void* offsets, const void* ck_codes,
+                              const void* ck_scales, const void* ck_y, void* dA, void* dW,
+                              void* dweights, void* workspace, void* stream);
 
 #ifdef __cplusplus
 }

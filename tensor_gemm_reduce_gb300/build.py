@@ -24,10 +24,10 @@ CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libgemm_rs.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("gemm_rs.cu", "block_norm.cu", "act8.cu", "backward.cu", "w4.cu", "fp8.cu",
-                                             "fp8_gemm.cu", "fp8_few.cu", "moe.cu")]
+                                             "fp8_gemm.cu", "fp8_gemm_f32.cu", "fp8_few.cu", "moe.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("kernels.cuh", "ptx.cuh", "schedule.h",
                                                   "ops_common.cuh", "act8.cuh",
-                                                  "tensor_pipe.cuh", "fp8.cuh", "mx.cuh")] + [
+                                                  "tensor_pipe.cuh", "fp8.cuh", "fp8_tiles.cuh", "mx.cuh")] + [
     os.path.join(ROOT, "include", f) for f in ("gemm_rs.h", "gemm_rs_ops.h")]
 
 BINDING_SOURCE = os.path.join(CSRC, "ops_binding.cpp")

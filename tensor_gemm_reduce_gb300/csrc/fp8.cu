@@ -2,11 +2,13 @@
 // include/gemm_rs_ops.h): quantisation to e4m3 with a scale for each block of 128,
 // and the layer's forward and backward pass from such codes.
 //
-// A block's scale is the least power of two, from 2^-126 on, whose 448-fold (448 is e4m3's
-// largest) is no less than its largest magnitude; a code is the element over the scale,
-// rounded to nearest even.  A power of two costs no precision of a code and is what the
-// tensor cores scale by themselves.  Blocks are 128 x 128 for
-// weights, 128 elements along the inner dimension of the product for activations
+// A block's scale is its largest magnitude over 448, e4m3's largest, in fp32; a code is the
+// element times the scale's reciprocal, rounded to nearest even.  Where the caller asks for it, it is
+// the least power of two, from 2^-126 on, whose 448-fold is no less than the largest magnitude, which
+// the tensor cores apply by themselves: 2048 x 8192 x 8192 takes half the time.  It costs accuracy, as a
+// block's largest then lies anywhere in the upper octave of the codes and off their grid: inputs with one
+// entry in 20 eight times as large are rounded by 2.7% of their norm, with fp32 by 2.1%.  Blocks are
+// 128 x 128 for weights, 128 elements along the inner dimension of the product for activations
 // and gradients: along a row for the forward pass and dA, along 128 tokens for dW.
 #include <cstring>
 
@@ -18,6 +20,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPairs = 76;  // of SMs
+// fp32 of 1 / 448, and the least magnitude that a block's largest counts as: an fp32 scale and its
+// reciprocal are normal numbers.
+constexpr float kPerLargest = (float)(1.0 / 448.0);
+constexpr float kSmallest = 7.888609052210118e-31f;  // 2^-100
+
 struct QuantizeParams {
   const uint4* x;
   long long x_plane;  // vectors of 8 between planes of x
@@ -28,10 +35,10 @@ struct QuantizeParams {
   const float* weights;
   int top_k;
   uint2* row_codes;
-  uint8_t* row_scales;
-  long long row_pitch;  // words of row_scales for four blocks
+  void* row_scales;
+  long long row_pitch;  // of row_scales: words for a block, bytes' words for four
   uint2* token_codes;
-  uint8_t* token_scales;
+  void* token_scales;
   long long padded;  // rows of token_codes in a plane
   int code_vec;                   // pitch of codes in vectors of 8
   uint32_t* status;
@@ -46,6 +53,12 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t top) {
 // 1 / scale, a power of two; NaN for 255.
 __device__ __forceinline__ float inverse_of(uint32_t scale) {
   return __uint_as_float(scale == 255u ? 0x7FC00000u : (254u - scale) << 23);
+}
+
+// The fp32 scale; NaN for infinities and NaN.
+__device__ __forceinline__ float scale_f32(uint32_t top) {
+  const float scale = fmaxf(__uint_as_float(top), kSmallest) * kPerLargest;
+  return top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : scale;
 }
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
@@ -129,12 +142,17 @@ __device__ __forceinline__ uint32_t product_codes4(uint64_t x, uint64_t ix, uint
                 __uint_as_float((uint32_t)(y >> 32)));
 }
 
+// Codes of four bf16 elements, pairs by pairs times their inverse scales in fp32.
+__device__ __forceinline__ uint32_t scaled4_f32(uint32_t x, uint64_t ix, uint32_t y, uint64_t iy) {
+  return product_codes4(pack_f32x2(bf16lo_to_f32(x), bf16hi_to_f32(x)), ix, pack_f32x2(bf16lo_to_f32(y), bf16hi_to_f32(y)), iy);
+}
+
 // A CTA's tile is 128 rows x 128 columns: a thread holds 8 columns of 8 rows, 16 rows
 // apart.  x is read once for both kinds of codes.  Bound by memory: 8192 x 28672 by rows
 // 100 us (7.0 TB/s), 4096 x 16384 of 8 experts both ways 52 us (5.1 TB/s).  Rows that are gathered
 // and weighted take `span` tiles a CTA, so that finding them is paid once (4096 x 6144: 42 us
 // with one, 29 with four).
-template <bool kRows, bool kTokens, bool kGather>
+template <bool kRows, bool kTokens, bool kGather, bool kE8m0>
 __global__ void __launch_bounds__(kThreads, kGather ? 2 : kTokens ? 3 : 4) quantize_kernel(const QuantizeParams p) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int spans = kGather ? (p.cb + p.span - 1) / p.span : p.cb;
@@ -208,22 +226,26 @@ __global__ void __launch_bounds__(kThreads, kGather ? 2 : kTokens ? 3 : 4) quant
       const int mine = tx & 7;
       uint32_t word = mine & 4 ? (mine & 2 ? top[3] : top[2]) : (mine & 2 ? top[1] : top[0]);
       word = mine & 1 ? word >> 16 : word & 0xFFFFu;
-      uint32_t scale, inverse;  // the inverse as a pair of bf16, or as fp32 where rows are weighted
+      word <<= 16;
       if constexpr (kGather) {
         float w = weight[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) w = mine == i ? weight[i] : w;
         // products by a weight are in the order of their factors
-        scale = scale_of(__float_as_uint(__fmul_rn(__uint_as_float(word << 16), w)) & 0x7FFFFFFFu);
-        inverse = __float_as_uint(inverse_of(scale));
-      } else {
-        scale = scale_of_bf16(word);
-        inverse = inverse_bf16(scale) * 0x10001u;
+        word = __float_as_uint(__fmul_rn(__uint_as_float(word), w)) & 0x7FFFFFFFu;
       }
-      const int my_row = row0 + ty + 16 * mine;
-      if (tx < 8 && my_row < end) {
-        const int block = plane * p.cb + cb;
-        p.row_scales[((block >> 2) * p.row_pitch + my_row) * 4 + (block & 3)] = (uint8_t)scale;
+      uint32_t inverse;  // as fp32; for bytes and rows that are not weighted as a pair of bf16
+      const int my_row = row0 + ty + 16 * mine, block = plane * p.cb + cb;
+      const bool stores = tx < 8 && my_row < end;
+      if constexpr (kE8m0) {
+        const uint32_t scale = scale_of(word);
+        inverse = kGather ? __float_as_uint(inverse_of(scale)) : inverse_bf16(scale) * 0x10001u;
+        if (stores)
+          static_cast<uint8_t*>(p.row_scales)[((block >> 2) * p.row_pitch + my_row) * 4 + (block & 3)] = (uint8_t)scale;
+      } else {
+        const float scale = scale_f32(word);
+        inverse = __float_as_uint(__frcp_rn(scale));
+        if (stores) static_cast<float*>(p.row_scales)[block * p.row_pitch + my_row] = scale;
       }
       uint2* out = p.row_codes + ((long long)plane * p.M + row0 + ty) * p.code_vec + col;
 #pragma unroll
@@ -231,9 +253,11 @@ __global__ void __launch_bounds__(kThreads, kGather ? 2 : kTokens ? 3 : 4) quant
         const uint32_t inv = __shfl_sync(0xffffffffu, inverse, half0 + i);
         if (row0 + ty + 16 * i >= end || !in) continue;
         uint2 codes;
+        const uint64_t f = pack_f32x2(__uint_as_float(inv), __uint_as_float(inv));
         if constexpr (kGather) {
-          const uint64_t f = pack_f32x2(__uint_as_float(inv), __uint_as_float(inv));
           codes = make_uint2(product_codes4(prod[i][0], f, prod[i][1], f), product_codes4(prod[i][2], f, prod[i][3], f));
+        } else if constexpr (!kE8m0) {
+          codes = make_uint2(scaled4_f32(raw[i].x, f, raw[i].y, f), scaled4_f32(raw[i].z, f, raw[i].w, f));
         } else {
           codes = make_uint2(scaled4(raw[i].x, inv, raw[i].y, inv), scaled4(raw[i].z, inv, raw[i].w, inv));
         }
@@ -244,7 +268,9 @@ __global__ void __launch_bounds__(kThreads, kGather ? 2 : kTokens ? 3 : 4) quant
       // each warp's largest of its 16 rows, then a column's by one thread
       const int warp = tid >> 5;
       uint2* out = p.token_codes + ((long long)plane * p.padded + rb * kBlk + ty) * p.code_vec + col;
-      uint8_t* scales = p.token_scales + ((long long)(rb >> 2) * p.planes + plane) * p.code_vec * 32 + (rb & 3);
+      // the first column's: a byte for every fourth, or fp32 each
+      uint8_t* bytes = static_cast<uint8_t*>(p.token_scales) + ((long long)(rb >> 2) * p.planes + plane) * p.code_vec * 32 + (rb & 3);
+      float* floats = static_cast<float*>(p.token_scales) + ((long long)rb * p.planes + plane) * p.code_vec * 8;
       if constexpr (kGather) {
         __shared__ uint32_t tops[kThreads / 32][kBlk];
         __shared__ float inverse[kBlk];
@@ -265,9 +291,15 @@ __global__ void __launch_bounds__(kThreads, kGather ? 2 : kTokens ? 3 : 4) quant
           uint32_t t = 0;
 #pragma unroll
           for (int w = 0; w < kThreads / 32; ++w) t = max(t, tops[w][tid]);
-          const uint32_t scale = scale_of(t);
-          inverse[tid] = inverse_of(scale);
-          if (in) scales[(col * 8 + ty) * 4ll] = (uint8_t)scale;
+          if constexpr (kE8m0) {
+            const uint32_t scale = scale_of(t);
+            inverse[tid] = inverse_of(scale);
+            if (in) bytes[(col * 8 + ty) * 4ll] = (uint8_t)scale;
+          } else {
+            const float scale = scale_f32(t);
+            inverse[tid] = __frcp_rn(scale);
+            if (in) floats[col * 8 + ty] = scale;
+          }
         }
         __syncthreads();
         if (in) {
@@ -281,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, kGather ? 2 : kTokens ? 3 : 4) quant
         }
       } else {
         __shared__ __align__(16) uint32_t tops[kThreads / 32][kBlk / 2];  // pairs of columns
-        __shared__ __align__(16) uint32_t inverse[kBlk / 2];
+        __shared__ __align__(16) uint32_t inverse[kE8m0 ? kBlk / 2 : kBlk];  // pairs of bf16, or fp32
         uint32_t top[4] = {};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -297,16 +329,33 @@ __global__ void __launch_bounds__(kThreads, kGather ? 2 : kTokens ? 3 : 4) quant
           uint32_t t = 0;
 #pragma unroll
           for (int w = 0; w < kThreads / 32; ++w) t = max_pairs(t, tops[w][tid]);
-          const uint32_t lo = scale_of_bf16(t & 0xFFFFu), hi = scale_of_bf16(t >> 16);
-          inverse[tid] = inverse_bf16(lo) | inverse_bf16(hi) << 16;
           const int c = cb * kBlk + 2 * tid;
-          if (c < p.vec * 8) {
-            scales[c * 4ll] = (uint8_t)lo;
-            scales[c * 4ll + 4] = (uint8_t)hi;
+          if constexpr (kE8m0) {
+            const uint32_t lo = scale_of_bf16(t & 0xFFFFu), hi = scale_of_bf16(t >> 16);
+            inverse[tid] = inverse_bf16(lo) | inverse_bf16(hi) << 16;
+            if (c < p.vec * 8) {
+              bytes[c * 4ll] = (uint8_t)lo;
+              bytes[c * 4ll + 4] = (uint8_t)hi;
+            }
+          } else {
+            const float lo = scale_f32(t << 16), hi = scale_f32(t & 0xFFFF0000u);
+            inverse[2 * tid] = __float_as_uint(__frcp_rn(lo));
+            inverse[2 * tid + 1] = __float_as_uint(__frcp_rn(hi));
+            if (c < p.vec * 8) *reinterpret_cast<float2*>(floats + c) = make_float2(lo, hi);
           }
         }
         __syncthreads();
-        if (in) {
+        if (in && !kE8m0) {
+          uint64_t inv[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            inv[j] = pack_f32x2(__uint_as_float(inverse[8 * tx + 2 * j]), __uint_as_float(inverse[8 * tx + 2 * j + 1]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            out[(long long)(16 * i) * p.code_vec] = make_uint2(scaled4_f32(raw[i].x, inv[0], raw[i].y, inv[1]),
+                                                               scaled4_f32(raw[i].z, inv[2], raw[i].w, inv[3]));
+        }
+        if (in && kE8m0) {
           const uint4 inv = *reinterpret_cast<const uint4*>(&inverse[4 * tx]);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -319,16 +368,25 @@ __global__ void __launch_bounds__(kThreads, kGather ? 2 : kTokens ? 3 : 4) quant
   }
 }
 
+template <bool kE8m0>
+auto quantizer(bool gather, bool rows, bool tokens) {
+  return gather ? (tokens ? (rows ? quantize_kernel<true, true, true, kE8m0> : quantize_kernel<false, true, true, kE8m0>)
+                          : quantize_kernel<true, false, true, kE8m0>)
+                : (tokens ? (rows ? quantize_kernel<true, true, false, kE8m0> : quantize_kernel<false, true, false, kE8m0>)
+                          : quantize_kernel<true, false, false, kE8m0>);
+}
+
 // Weights: one scale for the CTA's 128 x 128 tile, whose codes are 16 KB in a row (rows of 128
 // bytes, 8 KB apart in a weight of 8192 columns, were read at 4.7 TB/s where SMs read
 // different parts of it).  Bound by memory: 8 x 16384 x 6144 332 us, 7.3 TB/s.
 struct WeightParams {
   const uint4* w;
   uint2* codes;
-  uint8_t* scales;
+  void* scales;
   int Kr, vec, kb, nb;
 };
 
+template <bool kE8m0>
 __global__ void __launch_bounds__(kThreads) quantize_weight_kernel(const WeightParams p) {
   __shared__ uint32_t tops[kThreads / 32];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -361,14 +419,24 @@ __global__ void __launch_bounds__(kThreads) quantize_weight_kernel(const WeightP
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) top = max(top, tops[w]);
-  const uint32_t scale = scale_of_bf16(top), inv = inverse_bf16(scale) * 0x10001u;
-  if (tid == 0) p.scales[block] = (uint8_t)scale;
+  uint32_t inv;  // a pair of bf16, or fp32
+  if constexpr (kE8m0) {
+    const uint32_t scale = scale_of_bf16(top);
+    inv = inverse_bf16(scale) * 0x10001u;
+    if (tid == 0) static_cast<uint8_t*>(p.scales)[block] = (uint8_t)scale;
+  } else {
+    const float scale = scale_f32(top << 16);
+    inv = __float_as_uint(__frcp_rn(scale));
+    if (tid == 0) static_cast<float*>(p.scales)[block] = scale;
+  }
+  const uint64_t f = pack_f32x2(__uint_as_float(inv), __uint_as_float(inv));
   // the block's rows follow one another; columns behind the last are zero
   uint2* out = p.codes + ((plane * p.nb + nb) * p.Kr + row0) * 16 + tid;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (row0 + ty + 16 * i < p.Kr)
-      out[256 * i] = make_uint2(scaled4(raw[i].x, inv, raw[i].y, inv), scaled4(raw[i].z, inv, raw[i].w, inv));
+      out[256 * i] = kE8m0 ? make_uint2(scaled4(raw[i].x, inv, raw[i].y, inv), scaled4(raw[i].z, inv, raw[i].w, inv))
+                           : make_uint2(scaled4_f32(raw[i].x, f, raw[i].y, f), scaled4_f32(raw[i].z, f, raw[i].w, f));
 }
 
 // Parts that the contraction of a forward pass is cut in where its tiles are few: of those that run
@@ -500,45 +568,67 @@ int grs::fp8_quantize_rows(const Fp8Quantize& q, cudaStream_t st) {
     p.span = (int)(span < 1 ? 1 : span > 4 ? 4 : span);
   }
   const dim3 grid((unsigned)((int64_t)p.planes * p.rb * ((p.cb + p.span - 1) / p.span)));
-  auto kernel = gather ? (tokens ? (rows ? quantize_kernel<true, true, true> : quantize_kernel<false, true, true>)
-                                 : quantize_kernel<true, false, true>)
-                       : (tokens ? (rows ? quantize_kernel<true, true, false> : quantize_kernel<false, true, false>)
-                                 : quantize_kernel<true, false, false>);
+  const bool e8m0 = q.scale == kFp8E8m0;
+  auto kernel = e8m0 ? quantizer<true>(gather, rows, tokens) : quantizer<false>(gather, rows, tokens);
   return launch_overlapped(kernel, grid, kThreads, 0, st, p);
 }
 
-extern "C" int gemm_rs_fp8_weight_bytes(int64_t experts, int64_t N, int64_t K, size_t* code_bytes, size_t* scale_bytes) {
+namespace {
+
+int weight_bytes(Fp8Scale scale, int64_t experts, int64_t N, int64_t K, size_t* code_bytes, size_t* scale_bytes) {
   if (N < 0 || K < 0 || N % 8 || K % 64) return GEMM_RS_ERR_UNSUPPORTED_SHAPE;
   const int rc = fp8_check_sizes(0, experts, N, K);
   if (rc) return rc;
   const int64_t Kr = K / kWorld;
   if (code_bytes) *code_bytes = (size_t)experts * K * blocks_of(N) * kBlk;
-  if (scale_bytes) *scale_bytes = (size_t)experts * kWorld * blocks_of(Kr) * blocks_of(N);
+  if (scale_bytes) *scale_bytes = (size_t)experts * kWorld * blocks_of(Kr) * blocks_of(N) * (scale == kFp8F32 ? 4 : 1);
   return GEMM_RS_OK;
 }
 
-extern "C" int gemm_rs_fp8_quantize(int64_t experts, int64_t N, int64_t K, const void* W, void* codes, void* scales,
-                                    void* stream) {
+// fp32 scales are aligned as every buffer is; bytes may lie anywhere.
+bool misaligned_scales(Fp8Scale scale, const void* scales) { return scale == kFp8F32 && misaligned16(scales); }
+
+int quantize(Fp8Scale scale, int64_t experts, int64_t N, int64_t K, const void* W, void* codes, void* scales, void* stream) {
   size_t bytes = 0;
-  int rc = gemm_rs_fp8_weight_bytes(experts, N, K, &bytes, nullptr);
+  int rc = weight_bytes(scale, experts, N, K, &bytes, nullptr);
   if (rc) return rc;
   if (bytes == 0) return GEMM_RS_OK;
   if (!W || !codes || !scales) return GEMM_RS_ERR_INVALID_ARG;
   for (const void* q : {W, (const void*)codes})
     if (misaligned16(q)) return GEMM_RS_ERR_MISALIGNED;
+  if (misaligned_scales(scale, scales)) return GEMM_RS_ERR_MISALIGNED;
   int sms = 0;
   rc = current_device_sms(&sms);
   if (rc) return rc;
   WeightParams p;
   p.w = static_cast<const uint4*>(W);
   p.codes = static_cast<uint2*>(codes);
-  p.scales = static_cast<uint8_t*>(scales);
+  p.scales = scales;
   p.Kr = (int)(K / kWorld);
   p.vec = (int)(N / 8);
   p.kb = (int)blocks_of(p.Kr);
   p.nb = (int)blocks_of(N);
   const dim3 grid((unsigned)(experts * kWorld * p.kb * p.nb));
-  return launch_overlapped(quantize_weight_kernel, grid, kThreads, 0, static_cast<cudaStream_t>(stream), p);
+  return launch_overlapped(scale == kFp8F32 ? quantize_weight_kernel<false> : quantize_weight_kernel<true>, grid, kThreads, 0,
+                           static_cast<cudaStream_t>(stream), p);
+}
+
+}  // namespace
+
+extern "C" int gemm_rs_fp8_weight_bytes(int64_t experts, int64_t N, int64_t K, size_t* code_bytes, size_t* scale_bytes) {
+  return weight_bytes(kFp8F32, experts, N, K, code_bytes, scale_bytes);
+}
+extern "C" int gemm_rs_fp8_weight_bytes_e8m0(int64_t experts, int64_t N, int64_t K, size_t* code_bytes,
+                                             size_t* scale_bytes) {
+  return weight_bytes(kFp8E8m0, experts, N, K, code_bytes, scale_bytes);
+}
+extern "C" int gemm_rs_fp8_quantize(int64_t experts, int64_t N, int64_t K, const void* W, void* codes, void* scales,
+                                    void* stream) {
+  return quantize(kFp8F32, experts, N, K, W, codes, scales, stream);
+}
+extern "C" int gemm_rs_fp8_quantize_e8m0(int64_t experts, int64_t N, int64_t K, const void* W, void* codes, void* scales,
+                                         void* stream) {
+  return quantize(kFp8E8m0, experts, N, K, W, codes, scales, stream);
 }
 
 extern "C" int gemm_rs_fp8_checkpoint_bytes(int64_t M, int64_t K, size_t* code_bytes, size_t* scale_bytes) {
@@ -557,8 +647,10 @@ extern "C" int gemm_rs_fp8_workspace(int64_t M, int64_t N, int64_t K, size_t* by
   return GEMM_RS_OK;
 }
 
-extern "C" int gemm_rs_fp8_forward(int64_t M, int64_t N, int64_t K, const void* A, const void* codes, const void* scales,
-                                   void* ck_codes, void* ck_scales, void* out, void* workspace, void* stream) {
+namespace {
+
+int forward(Fp8Scale scale, int64_t M, int64_t N, int64_t K, const void* A, const void* codes, const void* scales,
+            void* ck_codes, void* ck_scales, void* out, void* workspace, void* stream) {
   int rc = check_shape(M, N, K);
   if (rc) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -566,6 +658,7 @@ extern "C" int gemm_rs_fp8_forward(int64_t M, int64_t N, int64_t K, const void* 
   for (const void* q : {A, codes, (const void*)ck_codes, (const void*)ck_scales, (const void*)out,
                         (const void*)workspace})
     if (misaligned16(q)) return GEMM_RS_ERR_MISALIGNED;
+  if (misaligned_scales(scale, scales)) return GEMM_RS_ERR_MISALIGNED;
   if (!workspace) return GEMM_RS_ERR_WORKSPACE;
   if (M == 0 || K == 0) {  // nothing to multiply
     rc = clear(workspace, sizeof(uint32_t), st);
@@ -577,19 +670,21 @@ extern "C" int gemm_rs_fp8_forward(int64_t M, int64_t N, int64_t K, const void* 
   if (rc) return rc;
   const Places w = forward_places(M, N, K);
   Fp8Quantize q;
+  q.scale = scale;
   q.x = A;
   q.planes = kWorld;
   q.cols = K / kWorld;
   q.rows.M = M;
   q.row_codes = at<void>(workspace, w.row_codes);
-  q.row_scales = at<uint8_t>(workspace, w.row_scales);
+  q.row_scales = at<void>(workspace, w.row_scales);
   q.token_codes = ck_codes;
-  q.token_scales = static_cast<uint8_t*>(ck_scales);
+  q.token_scales = ck_scales;
   q.status = at<uint32_t>(workspace, 0);
   rc = fp8_quantize_rows(q, st);
   if (rc || N == 0) return rc;
-  if (fp8_few_serves(kFp8Forward, q.rows, N, K / kWorld, false, sms)) {
+  if (fp8_few_serves(kFp8Forward, scale, q.rows, N, K / kWorld, false, sms)) {
     Fp8Few f;
+    f.scale = scale;
     f.kind = kFp8Forward;
     f.N = N;
     f.Kr = K / kWorld;
@@ -597,12 +692,13 @@ extern "C" int gemm_rs_fp8_forward(int64_t M, int64_t N, int64_t K, const void* 
     f.a = q.row_codes;
     f.a_scale = q.row_scales;
     f.b = codes;
-    f.b_scale = static_cast<const uint8_t*>(scales);
+    f.b_scale = scales;
     f.out = out;
     f.status = q.status;
     return fp8_few(f, st);
   }
   Fp8Product p;
+  p.scale = scale;
   p.kind = kFp8Forward;
   p.N = N;
   p.Kr = K / kWorld;
@@ -610,7 +706,7 @@ extern "C" int gemm_rs_fp8_forward(int64_t M, int64_t N, int64_t K, const void* 
   p.a = q.row_codes;
   p.a_scale = q.row_scales;
   p.b = codes;
-  p.b_scale = static_cast<const uint8_t*>(scales);
+  p.b_scale = scales;
   p.out = out;
   p.status = q.status;
   p.parts = parts_of(M, N, K);
@@ -627,14 +723,14 @@ extern "C" int gemm_rs_fp8_forward(int64_t M, int64_t N, int64_t K, const void* 
   return launch_overlapped(sum_parts_kernel, dim3((unsigned)((s.vec + kThreads - 1) / kThreads)), kThreads, 0, st, s);
 }
 
-extern "C" int gemm_rs_fp8_backward(int64_t M, int64_t N, int64_t K, const void* dY, const void* codes,
-                                    const void* scales, const void* ck_codes, const void* ck_scales, void* dA, void* dW,
-                                    void* workspace, void* stream) {
+int backward(Fp8Scale scale, int64_t M, int64_t N, int64_t K, const void* dY, const void* codes, const void* scales,
+             const void* ck_codes, const void* ck_scales, void* dA, void* dW, void* workspace, void* stream) {
   int rc = check_shape(M, N, K);
   if (rc) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   for (const void* q : {dY, codes, ck_codes, ck_scales, (const void*)dA, (const void*)dW, (const void*)workspace})
     if (misaligned16(q)) return GEMM_RS_ERR_MISALIGNED;
+  if (misaligned_scales(scale, scales)) return GEMM_RS_ERR_MISALIGNED;
   if (!workspace) return GEMM_RS_ERR_WORKSPACE;
   if (M == 0 || N == 0 || K == 0) {  // an empty contraction
     rc = clear(workspace, sizeof(uint32_t), st);
@@ -649,23 +745,25 @@ extern "C" int gemm_rs_fp8_backward(int64_t M, int64_t N, int64_t K, const void*
   if (rc) return rc;
   const Places w = backward_places(M, N);
   Fp8Quantize q;
+  q.scale = scale;
   q.x = dY;
   q.planes = 1;
   q.cols = N;
   q.rows.M = M;
   if (dA) {
     q.row_codes = at<void>(workspace, w.row_codes);
-    q.row_scales = at<uint8_t>(workspace, w.row_scales);
+    q.row_scales = at<void>(workspace, w.row_scales);
   }
   if (dW) {
     q.token_codes = at<void>(workspace, w.token_codes);
-    q.token_scales = at<uint8_t>(workspace, w.token_scales);
+    q.token_scales = at<void>(workspace, w.token_scales);
   }
   q.status = at<uint32_t>(workspace, 0);
-  const bool few = dA && fp8_few_serves(kFp8InputGrad, q.rows, N, K / kWorld, dW != nullptr, sms);
+  const bool few = dA && fp8_few_serves(kFp8InputGrad, scale, q.rows, N, K / kWorld, dW != nullptr, sms);
   rc = fp8_quantize_rows(q, st);
   if (rc) return rc;
   Fp8Product p;
+  p.scale = scale;
   p.N = N;
   p.Kr = K / kWorld;
   p.rows = q.rows;
@@ -673,6 +771,7 @@ extern "C" int gemm_rs_fp8_backward(int64_t M, int64_t N, int64_t K, const void*
   Fp8Product g = p;
   if (few) {
     Fp8Few f;
+    f.scale = scale;
     f.kind = kFp8InputGrad;
     f.N = N;
     f.Kr = K / kWorld;
@@ -680,7 +779,7 @@ extern "C" int gemm_rs_fp8_backward(int64_t M, int64_t N, int64_t K, const void*
     f.a = q.row_codes;
     f.a_scale = q.row_scales;
     f.b = codes;
-    f.b_scale = static_cast<const uint8_t*>(scales);
+    f.b_scale = scales;
     f.out = dA;
     f.status = q.status;
     rc = fp8_few(f, st);
@@ -690,13 +789,13 @@ extern "C" int gemm_rs_fp8_backward(int64_t M, int64_t N, int64_t K, const void*
     p.a = q.row_codes;
     p.a_scale = q.row_scales;
     p.b = codes;
-    p.b_scale = static_cast<const uint8_t*>(scales);
+    p.b_scale = scales;
     p.out = dA;
   }
   if (dW) {
     g.kind = kFp8WeightGrad;
     g.a = ck_codes;
-    g.a_scale = static_cast<const uint8_t*>(ck_scales);
+    g.a_scale = ck_scales;
     g.b = q.token_codes;
     g.b_scale = q.token_scales;
     g.out = dW;
@@ -705,6 +804,28 @@ extern "C" int gemm_rs_fp8_backward(int64_t M, int64_t N, int64_t K, const void*
   if (dA && !few) return fp8_product(p, st);
   if (dW) return fp8_product(g, st);
   return rc;
+}
+
+}  // namespace
+
+extern "C" int gemm_rs_fp8_forward(int64_t M, int64_t N, int64_t K, const void* A, const void* codes, const void* scales,
+                                   void* ck_codes, void* ck_scales, void* out, void* workspace, void* stream) {
+  return forward(kFp8F32, M, N, K, A, codes, scales, ck_codes, ck_scales, out, workspace, stream);
+}
+extern "C" int gemm_rs_fp8_forward_e8m0(int64_t M, int64_t N, int64_t K, const void* A, const void* codes,
+                                        const void* scales, void* ck_codes, void* ck_scales, void* out, void* workspace,
+                                        void* stream) {
+  return forward(kFp8E8m0, M, N, K, A, codes, scales, ck_codes, ck_scales, out, workspace, stream);
+}
+extern "C" int gemm_rs_fp8_backward(int64_t M, int64_t N, int64_t K, const void* dY, const void* codes,
+                                    const void* scales, const void* ck_codes, const void* ck_scales, void* dA, void* dW,
+                                    void* workspace, void* stream) {
+  return backward(kFp8F32, M, N, K, dY, codes, scales, ck_codes, ck_scales, dA, dW, workspace, stream);
+}
+extern "C" int gemm_rs_fp8_backward_e8m0(int64_t M, int64_t N, int64_t K, const void* dY, const void* codes,
+                                         const void* scales, const void* ck_codes, const void* ck_scales, void* dA,
+                                         void* dW, void* workspace, void* stream) {
+  return backward(kFp8E8m0, M, N, K, dY, codes, scales, ck_codes, ck_scales, dA, dW, workspace, stream);
 }
 
 extern "C" int gemm_rs_fp8_status(const void* workspace, void* stream) {

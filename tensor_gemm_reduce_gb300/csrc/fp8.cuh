@@ -31,20 +31,25 @@ struct Fp8Rows {
   int top_k = 1;
 };
 
+// What a block's scale is: fp32 of its largest magnitude over 448, or the least power of two that
+// holds it (a byte, its exponent).
+enum Fp8Scale { kFp8F32 = 0, kFp8E8m0 = 1 };
+
 // e4m3 codes of x [planes][M][cols] bf16.  By rows: 1 x 128 blocks along cols, codes
-// [planes][M][pitch]; a word of scales for each row and four of the planes * ceil(cols/128)
-// blocks.  By tokens: blocks of 128 rows of an expert, codes [planes][padded rows][pitch]; a word
-// of scales for each four blocks, plane and column.  Either may be absent.  status (if not null)
-// is set to zero.
+// [planes][M][pitch]; a scale for each of the planes * ceil(cols/128) blocks and row.  By tokens:
+// blocks of 128 rows of an expert, codes [planes][padded rows][pitch]; a scale for each block, plane
+// and column.  Bytes lie in words for four blocks.  Either may be absent.  status (if not null) is
+// set to zero.
 struct Fp8Quantize {
   const void* x;
   int planes;
   int64_t cols;
   Fp8Rows rows;
+  Fp8Scale scale;
   void* row_codes = nullptr;
-  uint8_t* row_scales = nullptr;    // [ceil(blocks / 4)][row_scale_pitch(M)][4]
+  void* row_scales = nullptr;    // fp32 [blocks][row_scale_pitch(M)], bytes [ceil(blocks / 4)][row_scale_pitch(M)][4]
   void* token_codes = nullptr;
-  uint8_t* token_scales = nullptr;  // [ceil(blocks / 4)][planes][pitch][4]
+  void* token_scales = nullptr;  // fp32 [blocks][planes][pitch], bytes [ceil(blocks / 4)][planes][pitch][4]
   uint32_t* status = nullptr;
 };
 int fp8_quantize_rows(const Fp8Quantize& q, cudaStream_t stream);
@@ -58,9 +63,10 @@ __device__ __forceinline__ int expert_row(const int* offsets, int e, int M) {
 }
 
 inline int64_t row_scale_pitch(int64_t M) { return (M + 3) / 4 * 4; }
-inline size_t row_scale_bytes(int64_t M, int64_t blocks) { return (size_t)((blocks + 3) / 4) * row_scale_pitch(M) * 4; }
+// Bytes of the scales of either kind: fp32's are the more.
+inline size_t row_scale_bytes(int64_t M, int64_t blocks) { return (size_t)blocks * row_scale_pitch(M) * 4; }
 inline size_t token_scale_bytes(int64_t rows, int planes, int64_t cols) {
-  return (size_t)((rows / kBlk + 3) / 4) * planes * fp8_pitch(cols) * 4;
+  return (size_t)(rows / kBlk) * planes * fp8_pitch(cols) * 4;
 }
 
 enum Fp8Kind { kFp8Forward = 0, kFp8InputGrad = 1, kFp8WeightGrad = 2 };
@@ -71,20 +77,29 @@ enum Fp8Kind { kFp8Forward = 0, kFp8InputGrad = 1, kFp8WeightGrad = 2 };
 //   weight grad  out[e][r][k][n] = sum_m a[r][m][k] b[m][n]   over the expert's padded rows
 struct Fp8Product {
   Fp8Kind kind;
+  Fp8Scale scale;
   int64_t N, Kr;
   Fp8Rows rows;
   const void* a;          // codes: forward [8][M][pitch(Kr)], input grad [M][pitch(N)], weight grad [8][padded][pitch(Kr)]
-  const uint8_t* a_scale;  // as fp8_quantize_rows lays them out
+  const void* a_scale;    // as fp8_quantize_rows lays them out
   const void* b;          // codes: the weight [e][8][ceil(N/128)][Kr][128]; weight grad [padded][pitch(N)]
-  const uint8_t* b_scale; // the weight's bytes [e][8][ceil(Kr/128)][ceil(N/128)]; weight grad: as a's
+  const void* b_scale;    // the weight's [e][8][ceil(Kr/128)][ceil(N/128)]; weight grad: as a's
   void* out;
   bool out_f32 = false;   // forward only
   int parts = 1;          // forward of one weight, into fp32: [parts][M][N], a run of the contraction each
   uint32_t* status;
 };
-int fp8_product(const Fp8Product& p, cudaStream_t stream);
+int fp8_product_f32(const Fp8Product& p, cudaStream_t stream);
+int fp8_product_e8m0(const Fp8Product& p, cudaStream_t stream);
+inline int fp8_product(const Fp8Product& p, cudaStream_t stream) {
+  return p.scale == kFp8F32 ? fp8_product_f32(p, stream) : fp8_product_e8m0(p, stream);
+}
 // dA and dW of the same rows in one launch.
-int fp8_products(const Fp8Product& input, const Fp8Product& weight, cudaStream_t stream);
+int fp8_products_f32(const Fp8Product& input, const Fp8Product& weight, cudaStream_t stream);
+int fp8_products_e8m0(const Fp8Product& input, const Fp8Product& weight, cudaStream_t stream);
+inline int fp8_products(const Fp8Product& input, const Fp8Product& weight, cudaStream_t stream) {
+  return input.scale == kFp8F32 ? fp8_products_f32(input, weight, stream) : fp8_products_e8m0(input, weight, stream);
+}
 
 // The forward product or dA for few rows, which reads each weight once: out [M][N] or
 // [8][M][Kr], or for experts' forward out [tokens][N] = sum_j weights[t][j] y[place[t][j]], y also
@@ -92,12 +107,13 @@ int fp8_products(const Fp8Product& input, const Fp8Product& weight, cudaStream_t
 constexpr int kFewRows = 128;
 struct Fp8Few {
   Fp8Kind kind;
+  Fp8Scale scale;
   int64_t N, Kr;
   Fp8Rows rows;
   const void* a;
-  const uint8_t* a_scale;
+  const void* a_scale;
   const void* b;
-  const uint8_t* b_scale;
+  const void* b_scale;
   void* out;
   int64_t tokens = 0;             // experts' forward: of out, top_k rows each
   const float* weights = nullptr; // [tokens][top_k]
@@ -107,7 +123,7 @@ struct Fp8Few {
 };
 // Whether fp8_few takes less time than fp8_product; with_weight_grad: dA beside which dW is wanted too,
 // which fp8_products would multiply in the same launch.
-bool fp8_few_serves(Fp8Kind kind, const Fp8Rows& rows, int64_t N, int64_t Kr, bool with_weight_grad, int sms);
+bool fp8_few_serves(Fp8Kind kind, Fp8Scale scale, const Fp8Rows& rows, int64_t N, int64_t Kr, bool with_weight_grad, int sms);
 int fp8_few(const Fp8Few& p, cudaStream_t stream);
 
 }  // namespace grs

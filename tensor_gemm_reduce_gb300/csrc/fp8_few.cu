@@ -26,15 +26,17 @@ using namespace grs;
 namespace {
 
 constexpr int kThreads = 256;
+// Scales.  Bytes: kSlots slots in shared memory and in TMEM, of four steps each.  fp32: kSteps slots in
+// shared memory, of one step each, and as many steps' sums in TMEM as fit.
 constexpr int kSlots = 4, kPerSlot = 4, kSfBytes = 512, kSlotBytes = 2 * kSfBytes;
+constexpr int kSteps = 8, kSums = 4;
 constexpr int kScaleBatch = 4;
 constexpr int kWeightBytes = kBlk * 128;
 constexpr uint64_t kLimitNs = 2000000000ull;  // of every wait
 
 struct Params {
   CUtensorMap tok, w;
-  const uint32_t* tok_scale;
-  const uint8_t* w_scale;
+  const void *tok_scale, *w_scale;
   const int* offsets;
   void* out;
   const float* weights;
@@ -53,13 +55,15 @@ struct Layout {
   static constexpr int kScales = kStages * kStageBytes;
   static constexpr int kPartial = kScales + kSlots * kSlotBytes;
   static constexpr int kBar = kPartial + kRows * 128 * 4;
-  static constexpr int kNumBars = 2 * kStages + 2 * kSlots + 5;  // full, empty, sf_full, sf_empty, acc_full[2], acc_empty[2], drain
+  // full, empty, sf_full, sf_empty, acc_full, acc_empty, drain
+  static constexpr int kNumBars = 2 * kStages + 2 * kSteps + 2 * kSums + 1;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kList = kMisc + 16;
   static constexpr int kAlloc = kList + kRows * 12 + 1024;
   static constexpr int kTmemScales = 2 * kRows;
   static constexpr int kTmemColumns = kRows == 16 ? 64 : kRows == 32 ? 128 : 256 + 256 * (kRows == 128);
-  static_assert(kTmemScales + kSlots * 8 <= kTmemColumns, "TMEM");
+  static_assert(kTmemScales + kSlots * 8 <= kTmemColumns && kSums * kRows <= kTmemColumns, "TMEM");
+  static_assert(kSteps * kRows * 4 <= kSlots * kSlotBytes, "fp32 scales");
   static_assert(kRows == 128 ? kAlloc <= 232448 : 2 * (kAlloc + 1024) <= 233472, "shared memory of an SM");
 };
 
@@ -68,7 +72,17 @@ struct Active {
   int e, row0, rows;
 };
 
-template <int kKind, int kRows>
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int kKind, int kRows, bool kE8m0>
 __global__ void __launch_bounds__(kThreads, kRows == 128 ? 1 : 2) fp8_few_kernel(const __grid_constant__ Params p) {
   using L = Layout<kRows>;
   extern __shared__ uint8_t smem_raw[];
@@ -81,10 +95,10 @@ __global__ void __launch_bounds__(kThreads, kRows == 128 ? 1 : 2) fp8_few_kernel
   const uint32_t bar_full = sbase + L::kBar;
   const uint32_t bar_empty = bar_full + 8 * L::kStages;
   const uint32_t bar_sf_full = bar_empty + 8 * L::kStages;
-  const uint32_t bar_sf_empty = bar_sf_full + 8 * kSlots;
-  const uint32_t bar_acc_full = bar_sf_empty + 8 * kSlots;
-  const uint32_t bar_acc_empty = bar_acc_full + 16;
-  const uint32_t bar_drain = bar_acc_empty + 16;
+  const uint32_t bar_sf_empty = bar_sf_full + 8 * kSteps;
+  const uint32_t bar_acc_full = bar_sf_empty + 8 * kSteps;
+  const uint32_t bar_acc_empty = bar_acc_full + 8 * kSums;
+  const uint32_t bar_drain = bar_acc_empty + 8 * kSums;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* cta_abort = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
   int* count = reinterpret_cast<int*>(smem + L::kMisc + 8);
@@ -95,11 +109,11 @@ __global__ void __launch_bounds__(kThreads, kRows == 128 ? 1 : 2) fp8_few_kernel
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
-    for (int s = 0; s < kSlots; ++s) {
+    for (int s = 0; s < kSteps; ++s) {
       mbar_init(bar_sf_full + 8 * s, 1);
-      mbar_init(bar_sf_empty + 8 * s, 1);
+      mbar_init(bar_sf_empty + 8 * s, kE8m0 ? 1 : 4);  // an MMA commit, or the warps that read the sums
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kSums; ++b) {
       mbar_init(bar_acc_full + 8 * b, 1);
       mbar_init(bar_acc_empty + 8 * b, 4);
     }
@@ -200,13 +214,44 @@ __global__ void __launch_bounds__(kThreads, kRows == 128 ? 1 : 2) fp8_few_kernel
     // --------------------------------------------------------------- MMA issuer
     const bool leader = elect_one();
     constexpr bool a_mn = kKind == kFp8Forward;
-    constexpr uint32_t idesc = idesc_mx(kBlk, kRows, a_mn, 0), a_step = a_mn ? 256 : 2;
+    constexpr uint32_t idesc = kE8m0 ? idesc_mx(kBlk, kRows, a_mn, 0) : idesc_e4m3(kBlk, kRows, a_mn, 0), a_step = a_mn ? 256 : 2;
     const uint64_t desc0 = smem_desc_sw128(sbase, 16, 1024);
     const uint32_t hi = (uint32_t)(desc0 >> 32);
     const uint64_t sf_desc = scales_desc(sbase + L::kScales);
     int stage = 0, slot = 0, buf = 0;
     uint32_t phase = 0, sf_phase = 0;
     bool ok = true;
+    if constexpr (!kE8m0) {  // each step into sums of its own
+      const int total = n_active * (s_end - s_begin);
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      for (int g = 0; g < total; ++g) {
+        if (!wait_bar(bar_full + 8 * stage, phase, kLimitNs, cta_abort) ||
+            !wait_bar(bar_acc_empty + 8 * acc, acc_phase ^ 1u, kLimitNs, cta_abort)) {
+          *cta_abort = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a = (uint32_t)desc0 + (uint32_t)(stage * (L::kStageBytes >> 4));
+        const uint32_t b = a + (uint32_t)(kWeightBytes >> 4);
+        if (leader) {
+#pragma unroll
+          for (uint32_t j = 0; j < kBlk / 32; ++j)
+            mma_e4m3(tmem_base + acc * kRows, desc_join(a + a_step * j, hi), desc_join(b + 2 * j, hi), idesc, j != 0 ? 1u : 0u);
+          mma_commit<1>(bar_acc_full + 8 * acc);
+          mma_commit<1>(bar_empty + 8 * stage);
+        }
+        if (++stage == L::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++acc == kSums) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      ok = false;
+    }
     for (int i = 0; ok && i < n_active; ++i) {
       const int acc = i & 1;
       if (!wait_bar(bar_acc_empty + 8 * acc, ((i >> 1) & 1) ^ 1u, kLimitNs, cta_abort)) {
@@ -261,10 +306,67 @@ __global__ void __launch_bounds__(kThreads, kRows == 128 ? 1 : 2) fp8_few_kernel
   } else if (warp == 2) {
     // ------------------------------------------------------------------- scales
     griddep_wait();
+    constexpr int kWords = (kRows + 31) / 32;
+    if constexpr (!kE8m0) {
+      // a step's for each row, times the weight's
+      struct Step {
+        float w, tok[kWords];
+      } sf[kScaleBatch];
+      int i = 0, step = s_begin, slot = 0;
+      uint32_t phase = 0;
+      auto fetch = [&](Step* x) {
+        if (i >= n_active || s_begin == s_end) return false;
+        const Active a = active[i];
+        const float* w = static_cast<const float*>(p.w_scale);
+        x->w = load_f32(kKind == kFp8Forward ? w + ((long long)a.e * steps + step) * p.NB + tile
+                                             : w + ((long long)a.e * kWorld * p.KB + tile) * p.NB + step);
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          const int row = a.row0 + lane + 32 * j;
+          x->tok[j] = load_f32(static_cast<const float*>(p.tok_scale) + step * p.tok_stride + (row < p.M ? row : p.M - 1));
+        }
+        if (++step == s_end) {
+          step = s_begin;
+          ++i;
+        }
+        return true;
+      };
+      bool ok = true, more = true;
+      while (ok && more) {
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < kScaleBatch; ++j)
+          if (more) {
+            more = fetch(&sf[j]);
+            n += more;
+          }
+#pragma unroll
+        for (int j = 0; j < kScaleBatch; ++j) {
+          if (!ok || j >= n) continue;
+          int got = 0;
+          if (lane == 0) got = wait_bar(bar_sf_empty + 8 * slot, phase ^ 1u, kLimitNs, cta_abort) ? 1 : 0;
+          got = __shfl_sync(0xffffffffu, got, 0);
+          if (!got) {
+            if (lane == 0) *cta_abort = 1;
+            ok = false;
+            continue;
+          }
+#pragma unroll
+          for (int k = 0; k < kWords; ++k)
+            if (lane + 32 * k < kRows)
+              st_shared_u32(sbase + L::kScales + (slot * kRows + lane + 32 * k) * 4, __float_as_uint(sf[j].w * sf[j].tok[k]));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_sf_full + 8 * slot);
+          if (++slot == kSteps) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
     const int slot0 = s_begin / kPerSlot, slot1 = (s_end - 1) / kPerSlot;
     int i = 0, c = slot0, slot = 0;
     uint32_t phase = 0;
-    constexpr int kWords = (kRows + 31) / 32;
     struct Scales {
       uint32_t byte, tok[kWords];
     } sf[kScaleBatch];
@@ -274,13 +376,13 @@ __global__ void __launch_bounds__(kThreads, kRows == 128 ? 1 : 2) fp8_few_kernel
       int step = c * kPerSlot + (lane & 3);
       step = step < steps ? step : steps - 1;
       if constexpr (kKind == kFp8Forward)
-        x->byte = load_u8(p.w_scale + ((long long)a.e * steps + step) * p.NB + tile);
+        x->byte = load_u8(static_cast<const uint8_t*>(p.w_scale) + ((long long)a.e * steps + step) * p.NB + tile);
       else
-        x->byte = load_u8(p.w_scale + ((long long)a.e * kWorld * p.KB + tile) * p.NB + step);
+        x->byte = load_u8(static_cast<const uint8_t*>(p.w_scale) + ((long long)a.e * kWorld * p.KB + tile) * p.NB + step);
 #pragma unroll
       for (int j = 0; j < kWords; ++j) {
         const int row = a.row0 + lane + 32 * j;
-        x->tok[j] = load_u32(p.tok_scale + c * p.tok_stride + (row < p.M ? row : p.M - 1));
+        x->tok[j] = load_u32(static_cast<const uint32_t*>(p.tok_scale) + c * p.tok_stride + (row < p.M ? row : p.M - 1));
       }
       if (++c > slot1) {
         c = slot0;
@@ -288,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, kRows == 128 ? 1 : 2) fp8_few_kernel
       }
       return true;
     };
-    bool ok = true, more = true;
+    bool ok = kE8m0, more = true;
     while (ok && more) {
       int n = 0;
 #pragma unroll
@@ -331,7 +433,65 @@ __global__ void __launch_bounds__(kThreads, kRows == 128 ? 1 : 2) fp8_few_kernel
     const int q = warp & 3;
     float* partial = reinterpret_cast<float*>(smem + L::kPartial) + q * 32 + lane;
     griddep_wait();
-    for (int i = 0; i < n_active; ++i) {
+    if constexpr (!kE8m0) {
+      // a step's products of codes, scaled, to sums in registers: a lane's column (for dA: row) of the weights
+      int acc = 0, slot = 0;
+      uint32_t acc_phase = 0, phase = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < n_active; ++i) {
+        const Active a = active[i];
+        float sums[kRows];
+#pragma unroll
+        for (int c = 0; c < kRows; ++c) sums[c] = 0.f;
+        for (int s = s_begin; s < s_end; ++s) {
+          int got = 0;
+          if (lane == 0)
+            got = wait_bar(bar_sf_full + 8 * slot, phase, kLimitNs, cta_abort) &&
+                  wait_bar(bar_acc_full + 8 * acc, acc_phase, kLimitNs, cta_abort);
+          got = __shfl_sync(0xffffffffu, got, 0);
+          if (!got) {
+            if (lane == 0) *cta_abort = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kRows / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld_16_columns(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kRows + 16 * c), v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float4 f;
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                           : "r"(sbase + L::kScales + (slot * kRows + 16 * c + 4 * k) * 4));
+              sums[16 * c + 4 * k] = fmaf(__uint_as_float(v[4 * k]), f.x, sums[16 * c + 4 * k]);
+              sums[16 * c + 4 * k + 1] = fmaf(__uint_as_float(v[4 * k + 1]), f.y, sums[16 * c + 4 * k + 1]);
+              sums[16 * c + 4 * k + 2] = fmaf(__uint_as_float(v[4 * k + 2]), f.z, sums[16 * c + 4 * k + 2]);
+              sums[16 * c + 4 * k + 3] = fmaf(__uint_as_float(v[4 * k + 3]), f.w, sums[16 * c + 4 * k + 3]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar_acc_empty + 8 * acc);
+            mbar_arrive(bar_sf_empty + 8 * slot);
+          }
+          if (++acc == kSums) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
+          if (++slot == kSteps) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kRows; ++c)
+          if (ok && c < a.rows && a.row0 + c < kRows) partial[(a.row0 + c) * 128] = sums[c];
+      }
+    }
+    for (int i = 0; kE8m0 && i < n_active; ++i) {
       const Active a = active[i];
       const int acc = i & 1;
       int got = 0;
@@ -414,20 +574,24 @@ __global__ void __launch_bounds__(kThreads, kRows == 128 ? 1 : 2) fp8_few_kernel
   cluster_sync_shared();  // every CTA's shared memory has been read
 }
 
-template <int kKind, int kRows>
+template <int kKind, int kRows, bool kE8m0>
 int launch(const Params& p, int tiles, cudaStream_t st) {
   using L = Layout<kRows>;
   static SmemAllowed allowed;
-  if (!allowed.set(fp8_few_kernel<kKind, kRows>, L::kAlloc)) return GEMM_RS_ERR_CUDA;
-  return launch_cluster(fp8_few_kernel<kKind, kRows>, tiles * p.split, p.split, kThreads, L::kAlloc, st, p);
+  if (!allowed.set(fp8_few_kernel<kKind, kRows, kE8m0>, L::kAlloc)) return GEMM_RS_ERR_CUDA;
+  return launch_cluster(fp8_few_kernel<kKind, kRows, kE8m0>, tiles * p.split, p.split, kThreads, L::kAlloc, st, p);
 }
 
-template <int kKind>
+template <int kKind, bool kE8m0>
 int launch_rows(const Params& p, int rows, int tiles, cudaStream_t st) {
-  return rows == 16   ? launch<kKind, 16>(p, tiles, st)
-         : rows == 32 ? launch<kKind, 32>(p, tiles, st)
-         : rows == 64 ? launch<kKind, 64>(p, tiles, st)
-                      : launch<kKind, 128>(p, tiles, st);
+  return rows == 16   ? launch<kKind, 16, kE8m0>(p, tiles, st)
+         : rows == 32 ? launch<kKind, 32, kE8m0>(p, tiles, st)
+         : rows == 64 ? launch<kKind, 64, kE8m0>(p, tiles, st)
+                      : launch<kKind, 128, kE8m0>(p, tiles, st);
+}
+template <bool kE8m0>
+int launch_kind(bool forward, const Params& p, int rows, int tiles, cudaStream_t st) {
+  return forward ? launch_rows<kFp8Forward, kE8m0>(p, rows, tiles, st) : launch_rows<kFp8InputGrad, kE8m0>(p, rows, tiles, st);
 }
 
 // Of the accumulator, for M rows.
@@ -459,7 +623,7 @@ Grid grid_of(Fp8Kind kind, int64_t M, int64_t N, int64_t Kr, int sms) {
 // every expert in turn, there experts are side by side and a tile is 256 rows whatever it holds.
 // 128 x 28672 x 8192 forward 81 against 55 us, 128 x 8192 x 28672 61 against 73, one row 40 against 76;
 // 32 rows of 16 experts, 1024 x 8192, 63 against 33.
-bool grs::fp8_few_serves(Fp8Kind kind, const Fp8Rows& rows, int64_t N, int64_t Kr, bool with_weight_grad, int sms) {
+bool grs::fp8_few_serves(Fp8Kind kind, Fp8Scale scale, const Fp8Rows& rows, int64_t N, int64_t Kr, bool with_weight_grad, int sms) {
   if (rows.M > kFewRows) return false;
   const int64_t E = rows.offsets ? rows.experts : 1;
   // up to 32 M weights one launch for both gradients is faster (128 x 2048 x 4096 42 -> 17.5 us), above it the
@@ -485,7 +649,7 @@ int grs::fp8_few(const Fp8Few& d, cudaStream_t st) {
   const bool fwd = d.kind == kFp8Forward;
   Params p;
   memset(&p, 0, sizeof(p));
-  p.tok_scale = reinterpret_cast<const uint32_t*>(d.a_scale);
+  p.tok_scale = d.a_scale;
   p.w_scale = d.b_scale;
   p.offsets = d.rows.offsets;
   p.out = d.out;
@@ -509,5 +673,5 @@ int grs::fp8_few(const Fp8Few& d, cudaStream_t st) {
             : encode_map(&p.tok, u8, 1, d.a, N, M, 1, kBlk, rows, fp8_pitch(N))) ||
       !encode_map(&p.w, u8, 1, d.b, kBlk, Kr, kWorld * E * blocks_of(N), kBlk, kBlk, kBlk))
     return GEMM_RS_ERR_CUDA;
-  return fwd ? launch_rows<kFp8Forward>(p, rows, tiles, st) : launch_rows<kFp8InputGrad>(p, rows, tiles, st);
+  return d.scale == kFp8F32 ? launch_kind<false>(fwd, p, rows, tiles, st) : launch_kind<true>(fwd, p, rows, tiles, st);
 }

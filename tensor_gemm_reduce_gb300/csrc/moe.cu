@@ -1092,15 +1092,18 @@ extern "C" int gemm_rs_moe_workspace(const gemm_rs_moe_desc* d, size_t* bytes) {
   return GEMM_RS_OK;
 }
 
-extern "C" int gemm_rs_moe_forward(const gemm_rs_moe_desc* d, const void* A, const void* codes, const void* scales,
-                                   const void* weights, const void* rows, const void* offsets, void* ck_codes,
-                                   void* ck_scales, void* ck_y, void* out, void* workspace, void* stream) {
+namespace {
+
+int forward(Fp8Scale scale, const gemm_rs_moe_desc* d, const void* A, const void* codes, const void* scales,
+            const void* weights, const void* rows, const void* offsets, void* ck_codes, void* ck_scales, void* ck_y,
+            void* out, void* workspace, void* stream) {
   int rc = check_desc(d);
   if (rc) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   for (const void* q : {A, codes, weights, rows, offsets, (const void*)ck_codes, (const void*)ck_scales,
                         (const void*)ck_y, (const void*)out, (const void*)workspace})
     if (misaligned16(q)) return GEMM_RS_ERR_MISALIGNED;
+  if (scale == kFp8F32 && misaligned16(scales)) return GEMM_RS_ERR_MISALIGNED;
   if (!workspace) return GEMM_RS_ERR_WORKSPACE;
   const int64_t P = d->T * d->top_k;
   const bool some = P > 0 && d->K > 0;
@@ -1119,6 +1122,7 @@ extern "C" int gemm_rs_moe_forward(const gemm_rs_moe_desc* d, const void* A, con
   const Places w = forward_places(*d);
   float* y = ck_y ? static_cast<float*>(ck_y) : at<float>(workspace, w.y);
   Fp8Quantize q;
+  q.scale = scale;
   q.x = A;
   q.planes = kWorld;
   q.cols = d->K / kWorld;
@@ -1126,14 +1130,15 @@ extern "C" int gemm_rs_moe_forward(const gemm_rs_moe_desc* d, const void* A, con
   q.rows.experts = (int)d->E;
   q.rows.offsets = static_cast<const int*>(offsets);
   q.row_codes = at<void>(workspace, w.row_codes);
-  q.row_scales = at<uint8_t>(workspace, w.row_scales);
+  q.row_scales = at<void>(workspace, w.row_scales);
   q.token_codes = ck_codes;
-  q.token_scales = static_cast<uint8_t*>(ck_scales);
+  q.token_scales = ck_scales;
   q.status = at<uint32_t>(workspace, 0);
   rc = fp8_quantize_rows(q, st);
   if (rc || d->N == 0) return rc;
-  if (fp8_few_serves(kFp8Forward, q.rows, d->N, d->K / kWorld, false, sms)) {
+  if (fp8_few_serves(kFp8Forward, scale, q.rows, d->N, d->K / kWorld, false, sms)) {
     Fp8Few f;
+    f.scale = scale;
     f.kind = kFp8Forward;
     f.N = d->N;
     f.Kr = d->K / kWorld;
@@ -1142,7 +1147,7 @@ extern "C" int gemm_rs_moe_forward(const gemm_rs_moe_desc* d, const void* A, con
     f.a = q.row_codes;
     f.a_scale = q.row_scales;
     f.b = codes;
-    f.b_scale = static_cast<const uint8_t*>(scales);
+    f.b_scale = scales;
     f.out = out;
     f.tokens = d->T;
     f.weights = static_cast<const float*>(weights);
@@ -1152,6 +1157,7 @@ extern "C" int gemm_rs_moe_forward(const gemm_rs_moe_desc* d, const void* A, con
     return fp8_few(f, st);
   }
   Fp8Product m;
+  m.scale = scale;
   m.kind = kFp8Forward;
   m.N = d->N;
   m.Kr = d->K / kWorld;
@@ -1159,7 +1165,7 @@ extern "C" int gemm_rs_moe_forward(const gemm_rs_moe_desc* d, const void* A, con
   m.a = q.row_codes;
   m.a_scale = q.row_scales;
   m.b = codes;
-  m.b_scale = static_cast<const uint8_t*>(scales);
+  m.b_scale = scales;
   m.out = y;
   m.out_f32 = true;
   m.status = q.status;
@@ -1179,16 +1185,16 @@ extern "C" int gemm_rs_moe_forward(const gemm_rs_moe_desc* d, const void* A, con
                            st, c);
 }
 
-extern "C" int gemm_rs_moe_backward(const gemm_rs_moe_desc* d, const void* dout, const void* codes, const void* scales,
-                                    const void* weights, const void* rows, const void* pairs, const void* offsets,
-                                    const void* ck_codes, const void* ck_scales, const void* ck_y, void* dA, void* dW,
-                                    void* dweights, void* workspace, void* stream) {
+int backward(Fp8Scale scale, const gemm_rs_moe_desc* d, const void* dout, const void* codes, const void* scales,
+             const void* weights, const void* rows, const void* pairs, const void* offsets, const void* ck_codes,
+             const void* ck_scales, const void* ck_y, void* dA, void* dW, void* dweights, void* workspace, void* stream) {
   int rc = check_desc(d);
   if (rc) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   for (const void* q : {dout, codes, weights, rows, pairs, offsets, ck_codes, ck_scales, ck_y, (const void*)dA,
                         (const void*)dW, (const void*)dweights, (const void*)workspace})
     if (misaligned16(q)) return GEMM_RS_ERR_MISALIGNED;
+  if (scale == kFp8F32 && misaligned16(scales)) return GEMM_RS_ERR_MISALIGNED;
   if (!workspace) return GEMM_RS_ERR_WORKSPACE;
   const int64_t P = d->T * d->top_k;
   if (P == 0 || d->N == 0 || d->K == 0) {
@@ -1208,6 +1214,7 @@ extern "C" int gemm_rs_moe_backward(const gemm_rs_moe_desc* d, const void* dout,
   const Places w = backward_places(*d);
   if (dA || dW) {
     Fp8Quantize q;
+  q.scale = scale;
     q.x = dout;
     q.planes = 1;
     q.cols = d->N;
@@ -1219,17 +1226,18 @@ extern "C" int gemm_rs_moe_backward(const gemm_rs_moe_desc* d, const void* dout,
     q.rows.top_k = (int)d->top_k;
     if (dA) {
       q.row_codes = at<void>(workspace, w.row_codes);
-      q.row_scales = at<uint8_t>(workspace, w.row_scales);
+      q.row_scales = at<void>(workspace, w.row_scales);
     }
     if (dW) {
       q.token_codes = at<void>(workspace, w.token_codes);
-      q.token_scales = at<uint8_t>(workspace, w.token_scales);
+      q.token_scales = at<void>(workspace, w.token_scales);
     }
     q.status = at<uint32_t>(workspace, 0);
-    const bool few = dA && fp8_few_serves(kFp8InputGrad, q.rows, d->N, d->K / kWorld, dW != nullptr, sms);
+    const bool few = dA && fp8_few_serves(kFp8InputGrad, scale, q.rows, d->N, d->K / kWorld, dW != nullptr, sms);
     rc = fp8_quantize_rows(q, st);
     if (rc) return rc;
     Fp8Product m;
+  m.scale = scale;
     m.N = d->N;
     m.Kr = d->K / kWorld;
     m.rows = q.rows;
@@ -1237,6 +1245,7 @@ extern "C" int gemm_rs_moe_backward(const gemm_rs_moe_desc* d, const void* dout,
     Fp8Product g = m;
     if (few) {
       Fp8Few f;
+    f.scale = scale;
       f.kind = kFp8InputGrad;
       f.N = d->N;
       f.Kr = d->K / kWorld;
@@ -1244,7 +1253,7 @@ extern "C" int gemm_rs_moe_backward(const gemm_rs_moe_desc* d, const void* dout,
       f.a = q.row_codes;
       f.a_scale = q.row_scales;
       f.b = codes;
-      f.b_scale = static_cast<const uint8_t*>(scales);
+      f.b_scale = scales;
       f.out = dA;
       f.status = q.status;
       rc = fp8_few(f, st);
@@ -1254,13 +1263,13 @@ extern "C" int gemm_rs_moe_backward(const gemm_rs_moe_desc* d, const void* dout,
       m.a = q.row_codes;
       m.a_scale = q.row_scales;
       m.b = codes;
-      m.b_scale = static_cast<const uint8_t*>(scales);
+      m.b_scale = scales;
       m.out = dA;
     }
     if (dW) {
       g.kind = kFp8WeightGrad;
       g.a = ck_codes;
-      g.a_scale = static_cast<const uint8_t*>(ck_scales);
+      g.a_scale = ck_scales;
       g.b = q.token_codes;
       g.b_scale = q.token_scales;
       g.out = dW;
@@ -1287,4 +1296,32 @@ extern "C" int gemm_rs_moe_backward(const gemm_rs_moe_desc* d, const void* dout,
   c.pairs = P;
   const long long blocks = (P * 32 + kCombineThreads - 1) / kCombineThreads;
   return launch_overlapped(weight_grad_kernel, dim3((unsigned)blocks), kCombineThreads, 0, st, c);
+}
+
+}  // namespace
+
+extern "C" int gemm_rs_moe_forward(const gemm_rs_moe_desc* d, const void* A, const void* codes, const void* scales,
+                                   const void* weights, const void* rows, const void* offsets, void* ck_codes,
+                                   void* ck_scales, void* ck_y, void* out, void* workspace, void* stream) {
+  return forward(kFp8F32, d, A, codes, scales, weights, rows, offsets, ck_codes, ck_scales, ck_y, out, workspace, stream);
+}
+extern "C" int gemm_rs_moe_forward_e8m0(const gemm_rs_moe_desc* d, const void* A, const void* codes, const void* scales,
+                                        const void* weights, const void* rows, const void* offsets, void* ck_codes,
+                                        void* ck_scales, void* ck_y, void* out, void* workspace, void* stream) {
+  return forward(kFp8E8m0, d, A, codes, scales, weights, rows, offsets, ck_codes, ck_scales, ck_y, out, workspace, stream);
+}
+extern "C" int gemm_rs_moe_backward(const gemm_rs_moe_desc* d, const void* dout, const void* codes, const void* scales,
+                                    const void* weights, const void* rows, const void* pairs, const void* offsets,
+                                    const void* ck_codes, const void* ck_scales, const void* ck_y, void* dA, void* dW,
+                                    void* dweights, void* workspace, void* stream) {
+  return backward(kFp8F32, d, dout, codes, scales, weights, rows, pairs, offsets, ck_codes, ck_scales, ck_y, dA, dW, dweights,
+                  workspace, stream);
+}
+extern "C" int gemm_rs_moe_backward_e8m0(const gemm_rs_moe_desc* d, const void* dout, const void* codes,
+                                         const void* scales, const void* weights, const void* rows, const void* pairs,
+                                         const void* offsets, const void* ck_codes, const void* ck_scales,
+                                         const void* ck_y, void* dA, void* dW, void* dweights, void* workspace,
+                                         void* stream) {
+  return backward(kFp8E8m0, d, dout, codes, scales, weights, rows, pairs, offsets, ck_codes, ck_scales, ck_y, dA, dW,
+                  dweights, workspace, stream);
 }

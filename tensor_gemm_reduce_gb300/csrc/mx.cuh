@@ -51,6 +51,12 @@ __host__ __device__ constexpr uint32_t idesc_mx(int M, int N, int a_mn_major, in
 }
 __device__ __forceinline__ uint32_t idesc_step(uint32_t idesc, uint32_t id) { return idesc | (id << 4) | (id << 29); }
 
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator, e4m3 operands, no scales.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major, int b_mn_major) {
+  return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+
 // One lane of a converged warp.  Loops that issue MMAs run in whole warps, so that
 // their descriptors stay uniform, and this lane alone issues.
 __device__ __forceinline__ bool elect_one() {

@@ -254,6 +254,14 @@ PyObject* w4_matvec(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Whether the weight's scales are powers of two (e8m0), not fp32: which of the entries serves.
+bool powers_of_two(Call& c, PyObject* scales) {
+  const at::Tensor& t = c.tensor(scales, "the weight's scales");
+  if (t.scalar_type() != kF && t.scalar_type() != at::ScalarType::Float8_e8m0fnu)
+    type_error(std::string("the weight's scales must be Float or Float8_e8m0fnu, got ") + c10::toString(t.scalar_type()));
+  return t.scalar_type() != kF;
+}
+
 // W, codes, scales, stream
 PyObject* fp8_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 4, [&] {
@@ -262,13 +270,14 @@ PyObject* fp8_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if ((t.dim() != 3 && t.dim() != 4) || t.size(-3) != kWorld)
       value_error("W must have shape [8][K/8][N] or [E][8][K/8][N], got " + text(t.sizes()));
     const int64_t E = t.dim() == 4 ? t.size(0) : 1, N = t.size(-1), K = t.size(-2) * kWorld;
+    const bool e8m0 = powers_of_two(c, a[2]);
     size_t code_bytes = 0, scale_bytes = 0;
-    const int rc = gemm_rs_fp8_weight_bytes(E, N, K, &code_bytes, &scale_bytes);
+    const int rc = (e8m0 ? gemm_rs_fp8_weight_bytes_e8m0 : gemm_rs_fp8_weight_bytes)(E, N, K, &code_bytes, &scale_bytes);
     if (rc) return rc;
     void* W = c.in(a[0], kB, t.sizes(), "W");
     void* codes = c.buffer(a[1], code_bytes, "the weight's codes", true);
     void* scales = c.buffer(a[2], scale_bytes, "the weight's scales", true);
-    return gemm_rs_fp8_quantize(E, N, K, W, codes, scales, c.stream(a[3]));
+    return (e8m0 ? gemm_rs_fp8_quantize_e8m0 : gemm_rs_fp8_quantize)(E, N, K, W, codes, scales, c.stream(a[3]));
   });
 }
 
@@ -278,8 +287,9 @@ PyObject* fp8_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call c;
     const int64_t M = PyLong_AsLongLong(a[1]), N = PyLong_AsLongLong(a[2]), K = PyLong_AsLongLong(a[3]);
     size_t need = 0, code_bytes = 0, scale_bytes = 0, ck_codes = 0, ck_scales = 0;
+    const bool e8m0 = powers_of_two(c, a[5]);
     int rc = gemm_rs_fp8_workspace(M, N, K, &need);
-    if (!rc) rc = gemm_rs_fp8_weight_bytes(1, N, K, &code_bytes, &scale_bytes);
+    if (!rc) rc = (e8m0 ? gemm_rs_fp8_weight_bytes_e8m0 : gemm_rs_fp8_weight_bytes)(1, N, K, &code_bytes, &scale_bytes);
     if (!rc) rc = gemm_rs_fp8_checkpoint_bytes(M, K, &ck_codes, &ck_scales);
     if (rc) return rc;
     const int64_t as[3] = {kWorld, M, K / kWorld}, os[2] = {M, N};
@@ -290,7 +300,7 @@ PyObject* fp8_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* cs = a[7] == Py_None ? nullptr : c.buffer(a[7], ck_scales, "the checkpoint's scales", true);
     void* out = c.out(a[8], kB, os, "out");
     void* work = c.buffer(a[9], need, "workspace", true);
-    return gemm_rs_fp8_forward(M, N, K, A, wc, ws, cc, cs, out, work, c.stream(a[10]));
+    return (e8m0 ? gemm_rs_fp8_forward_e8m0 : gemm_rs_fp8_forward)(M, N, K, A, wc, ws, cc, cs, out, work, c.stream(a[10]));
   });
 }
 
@@ -300,8 +310,9 @@ PyObject* fp8_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call c;
     const int64_t M = PyLong_AsLongLong(a[1]), N = PyLong_AsLongLong(a[2]), K = PyLong_AsLongLong(a[3]);
     size_t need = 0, code_bytes = 0, scale_bytes = 0, ck_codes = 0, ck_scales = 0;
+    const bool e8m0 = powers_of_two(c, a[5]);
     int rc = gemm_rs_fp8_workspace(M, N, K, &need);
-    if (!rc) rc = gemm_rs_fp8_weight_bytes(1, N, K, &code_bytes, &scale_bytes);
+    if (!rc) rc = (e8m0 ? gemm_rs_fp8_weight_bytes_e8m0 : gemm_rs_fp8_weight_bytes)(1, N, K, &code_bytes, &scale_bytes);
     if (!rc) rc = gemm_rs_fp8_checkpoint_bytes(M, K, &ck_codes, &ck_scales);
     if (rc) return rc;
     const int64_t ys[2] = {M, N}, as[3] = {kWorld, M, K / kWorld}, ws_[3] = {kWorld, K / kWorld, N};
@@ -318,7 +329,8 @@ PyObject* fp8_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       dW = c.out(a[9], kB, ws_, "dW");
     }
     void* work = c.buffer(a[10], need, "workspace", true);
-    return gemm_rs_fp8_backward(M, N, K, dY, wc, ws, cc, cs, dA, dW, work, c.stream(a[11]));
+    return (e8m0 ? gemm_rs_fp8_backward_e8m0 : gemm_rs_fp8_backward)(M, N, K, dY, wc, ws, cc, cs, dA, dW, work,
+                                                                     c.stream(a[11]));
   });
 }
 
@@ -406,8 +418,9 @@ PyObject* moe_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call c;
     const gemm_rs_moe_desc d = moe_desc(a + 1);
     size_t need = 0, code_bytes = 0, scale_bytes = 0, ck_codes = 0, ck_scales = 0, ck_y = 0;
+    const bool e8m0 = powers_of_two(c, a[7]);
     int rc = gemm_rs_moe_workspace(&d, &need);
-    if (!rc) rc = gemm_rs_fp8_weight_bytes(d.E, d.N, d.K, &code_bytes, &scale_bytes);
+    if (!rc) rc = (e8m0 ? gemm_rs_fp8_weight_bytes_e8m0 : gemm_rs_fp8_weight_bytes)(d.E, d.N, d.K, &code_bytes, &scale_bytes);
     if (!rc) rc = gemm_rs_moe_checkpoint_bytes(&d, &ck_codes, &ck_scales, &ck_y);
     if (rc) return rc;
     const int64_t as[3] = {kWorld, d.T * d.top_k, d.K / kWorld}, ks[2] = {d.T, d.top_k}, es[1] = {d.E + 1},
@@ -424,7 +437,8 @@ PyObject* moe_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* cy = keep ? c.buffer(a[13], ck_y, "the checkpoint's y", true) : nullptr;
     void* out = c.out(a[14], kB, os, "out");
     void* work = c.buffer(a[15], need, "workspace", true);
-    return gemm_rs_moe_forward(&d, A, wc, ws, weights, rows, offsets, cc, cs, cy, out, work, c.stream(a[16]));
+    return (e8m0 ? gemm_rs_moe_forward_e8m0 : gemm_rs_moe_forward)(&d, A, wc, ws, weights, rows, offsets, cc, cs, cy, out,
+                                                                   work, c.stream(a[16]));
   });
 }
 
@@ -435,8 +449,9 @@ PyObject* moe_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call c;
     const gemm_rs_moe_desc d = moe_desc(a + 1);
     size_t need = 0, code_bytes = 0, scale_bytes = 0, ck_codes = 0, ck_scales = 0, ck_y = 0;
+    const bool e8m0 = powers_of_two(c, a[7]);
     int rc = gemm_rs_moe_workspace(&d, &need);
-    if (!rc) rc = gemm_rs_fp8_weight_bytes(d.E, d.N, d.K, &code_bytes, &scale_bytes);
+    if (!rc) rc = (e8m0 ? gemm_rs_fp8_weight_bytes_e8m0 : gemm_rs_fp8_weight_bytes)(d.E, d.N, d.K, &code_bytes, &scale_bytes);
     if (!rc) rc = gemm_rs_moe_checkpoint_bytes(&d, &ck_codes, &ck_scales, &ck_y);
     if (rc) return rc;
     const int64_t P = d.T * d.top_k, ds[2] = {d.T, d.N}, ks[2] = {d.T, d.top_k}, ps[1] = {P}, es[1] = {d.E + 1},
@@ -463,8 +478,8 @@ PyObject* moe_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       dw = c.out(a[17], kF, ks, "dweights");
     }
     void* work = c.buffer(a[18], need, "workspace", true);
-    return gemm_rs_moe_backward(&d, dout, wc, ws, weights, rows, pairs, offsets, cc, cs, cy, dA, dW, dw, work,
-                                c.stream(a[19]));
+    return (e8m0 ? gemm_rs_moe_backward_e8m0 : gemm_rs_moe_backward)(&d, dout, wc, ws, weights, rows, pairs, offsets, cc, cs,
+                                                                     cy, dA, dW, dw, work, c.stream(a[19]));
   });
 }
 

@@ -131,6 +131,7 @@ class Checkpoint:
         self.codes = torch.empty(cb.value, dtype=_U8, device=device)
         self.scales = torch.empty(sb.value, dtype=_U8, device=device)
         self.y = torch.empty(d.T * d.top_k, d.N, dtype=_F32, device=device)
+        self.scale_type = None  # as fp8.Checkpoint's
 
 
 def workspace_bytes(routing: Routing, weight: _f.Weight) -> int:
@@ -173,6 +174,8 @@ def forward(A, weight: _f.Weight, routing: Routing, checkpoint: Checkpoint = Non
                               *kept, out, workspace, None if stream is None else stream.cuda_stream)
     if rc:
         _a.check(rc, "gemm_rs_moe_forward")
+    if checkpoint is not None:
+        checkpoint.scale_type = weight.scales.dtype
     return out
 
 
@@ -188,6 +191,7 @@ def backward(dout, weight: _f.Weight, routing: Routing, checkpoint: Checkpoint, 
     if checkpoint is None and (dW is not None or dweights is not None):
         raise ValueError("dW and dweights need the checkpoint")
     key = _check(routing, weight, checkpoint)
+    _f.check_scale_type(checkpoint, weight)
     kept = (None, None, None) if checkpoint is None else (checkpoint.codes, checkpoint.scales, checkpoint.y)
     rc = _a.ops().moe_backward(dout, *key, weight.storage, weight.scales, routing.weights, routing.rows, routing.pairs,
                                routing.offsets, *kept, dA, dW, dweights, workspace,

@@ -68,6 +68,10 @@ SIGS = {
     "gemm_rs_fp8_workspace": [_L, _L, _L, _P],
     "gemm_rs_fp8_forward": [_L, _L, _L] + [_P] * 8,
     "gemm_rs_fp8_backward": [_L, _L, _L] + [_P] * 9,
+    "gemm_rs_fp8_weight_bytes_e8m0": [_L, _L, _L, _P, _P],
+    "gemm_rs_fp8_quantize_e8m0": [_L, _L, _L, _P, _P, _P, _P],
+    "gemm_rs_fp8_forward_e8m0": [_L, _L, _L] + [_P] * 8,
+    "gemm_rs_fp8_backward_e8m0": [_L, _L, _L] + [_P] * 9,
     "gemm_rs_fp8_status": [_P, _P],
     "gemm_rs_moe_route": [_P] * 10,
     "gemm_rs_moe_arrange": [_L, _L, _L] + [_P] * 5,
@@ -76,6 +80,8 @@ SIGS = {
     "gemm_rs_moe_workspace": [_P] * 2,
     "gemm_rs_moe_forward": [_P] * 13,
     "gemm_rs_moe_backward": [_P] * 16,
+    "gemm_rs_moe_forward_e8m0": [_P] * 13,
+    "gemm_rs_moe_backward_e8m0": [_P] * 16,
 }
 
 _LIB: Optional[ctypes.CDLL] = None
