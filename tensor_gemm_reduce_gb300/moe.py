@@ -32,15 +32,17 @@ _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 class Routing:
     """T tokens' k experts out of E (uninitialised): ids and weights [T][k], descending by
     choice; rows [T][k], each pair's place in the order of the experts (-1 without an expert);
-    pairs [T*k], the pair t*k + j at each place; offsets [E+1], each expert's first place and,
-    last, the number of pairs with an expert."""
+    pairs [T*k], the pair t*k + j at each place, and behind the last one with an expert 0 or what an
+    earlier call left there, so that every place is an index; offsets [E+1], each expert's first place
+    and, last, the number of pairs with an expert."""
 
     def __init__(self, T: int, k: int, E: int, device=None):
         self.T, self.k, self.E = int(T), int(k), int(E)
         device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
         self.ids, self.rows = (torch.empty(self.T, self.k, dtype=_I32, device=device) for _ in range(2))
         self.weights = torch.empty(self.T, self.k, dtype=_F32, device=device)
-        self.pairs = torch.empty(self.T * self.k, dtype=_I32, device=device)
+        # places behind the last pair with an expert are never written: they hold a pair that there is
+        self.pairs = torch.zeros(self.T * self.k, dtype=_I32, device=device)
         self.offsets = torch.empty(self.E + 1, dtype=_I32, device=device)
         self.options = None  # how route() chose: (score, groups, top_groups, renormalize, scale)
 

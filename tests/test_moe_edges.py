@@ -1,0 +1,51 @@
+"""Routing and the experts' layer where scores saturate, logits are not finite, choices tie at the
+border and tensors are empty in part, against the definitions in float64.
+
+Tolerances.  A routed weight is a quotient of exponentials of fp32 differences: an exponential is off
+by 2 units in the last place, 4 * 2**-24, its argument x by |x| * 2**-24; a score takes two of them, a sum
+and a quotient, the sum of up to 16 another 16 roundings: below 64 * 2**-24 of it for |x| up to 16, and in
+all 64 + |x|.  A sigmoid's gradient takes the complement of a score as well, two exponentials and two
+roundings more: 96 * 2**-24 of the terms that it is the difference of.
+"""
+import pytest
+import torch
+
+from tensor_gemm_reduce_gb300 import fp8, moe
+from tensor_gemm_reduce_gb300 import gemm_rs as G
+from test_fp8 import U, bits
+from test_moe import assert_arranged, call, chosen, experts, order
+
+BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def shares(logits, ids):
+    """The chosen sigmoids' shares of their sum, in float64 without underflow."""
+    l = logits.double().gather(1, ids.long())
+    return torch.softmax(-torch.nn.functional.softplus(-l), 1)
+
+
+LOW = [(3, 8, 2), (300, 8, 2), (300, 40, 6), (40, 200, 8)]
+
+
+@pytest.mark.gpu
+def test_the_places_of_a_padded_batch_are_indices():
+    """x[pairs // k], as the module's documentation has it, with masked tokens."""
+    taken = torch.full((1 << 20,), 1 << 30, dtype=I32, device="cuda")
+    del taken  # the allocator's memory, of which the routing is made
+    T, E, k = 1000, 8, 2
+    x, mask = bits(T, 64).cuda(), torch.arange(T) % 3 > 0
+    r = call(torch.randn(T, E, generator=torch.Generator().manual_seed(1)), k, {}, mask=mask)
+    assert ((r.pairs >= 0) & (r.pairs < T * k)).all()
+    used = int(r.offsets[-1])
+    rows, _, pairs = order(r.ids.cpu(), E)
+    assert torch.equal(x[r.pairs.long() // k][:used].cpu(), x.cpu()[pairs.long() // k])
+
+
+# ---------------------------------------------------------------- no GPU needed
+
+
+def test_a_new_routing_holds_places_of_the_tensors(monkeypatch):
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *s, **kw: empty(*s, **kw).fill_(1 << 20))
+    r = moe.Routing(5, 2, 4, device="cpu")
+    assert ((r.pairs >= 0) & (r.pairs < 10)).all()
