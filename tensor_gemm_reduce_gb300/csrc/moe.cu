@@ -105,6 +105,13 @@ __device__ __forceinline__ void lanes_best(unsigned long long& key, int& index) 
 __device__ __forceinline__ float exp_of(float v) { return expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
 
+// sigmoid(x) / e^top where top, no less than x, is negative, else sigmoid(x): scores that are divided by
+// their sum keep their ratios where each would underflow.
+__device__ __forceinline__ float sigmoid_over(float x, float top) {
+  if (x >= 0.f) return 1.f / (1.f + expf(-x));
+  return top == -INFINITY ? 0.f : expf(x - fminf(top, 0.f)) / (1.f + expf(x));
+}
+
 // Scores of a token from its logits (E of them, slots behind E hold -inf).
 template <int W, typename F, int kPer>
 __device__ __forceinline__ void scores_of(const float (&logit)[kPer], bool sigmoid, F (&score)[kPer]) {
@@ -313,11 +320,9 @@ __device__ __forceinline__ void route_tokens(const RouteParams& p, int t0, int l
   float mine = values[id];
   __syncwarp();
   const bool in = sub < p.top_k;
-  if (p.sigmoid) {
-    mine = 1.f / (1.f + expf(-mine));
-  } else if (p.renormalize) {
-    const float top = lanes_max<W>(in ? mine : -INFINITY);
-    mine = top == -INFINITY ? 0.f : expf(mine - top);
+  if (p.sigmoid || p.renormalize) {
+    const float top = p.renormalize ? lanes_max<W>(in ? mine : -INFINITY) : 0.f;
+    mine = p.sigmoid ? sigmoid_over(mine, top) : top == -INFINITY ? 0.f : expf(mine - top);
   }
   float total = 1.f;
   if (p.renormalize) {
@@ -729,19 +734,17 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
   }
   scores_of<W>(logit, p.sigmoid, score);
   const bool has = (unsigned)id < (unsigned)p.E;
-  // the chosen one's score, or its logit where the others cancel
-  const bool softmax_of_chosen = p.renormalize && !p.sigmoid;
+  // the chosen one's score, or its logit where it is a share of the chosen ones' sum
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) values[sub + W * i] = softmax_of_chosen ? logit[i] : score[i];
+  for (int i = 0; i < kPer; ++i) values[sub + W * i] = p.renormalize ? logit[i] : score[i];
   __syncwarp();
-  const float s = has ? values[id] : softmax_of_chosen ? -INFINITY : 0.f;
+  float s = has ? values[id] : p.renormalize ? -INFINITY : 0.f;
   __syncwarp();
   float u = s;
   if (p.renormalize) {
-    if (!p.sigmoid) {
-      const float top = lanes_max<W>(s);
-      u = top == -INFINITY || !has ? 0.f : expf(s - top);
-    }
+    const float top = lanes_max<W>(s);
+    u = top == -INFINITY || !has ? 0.f : p.sigmoid ? sigmoid_over(s, top) : expf(s - top);
+    if (p.sigmoid) s = sigmoid_over(s, 0.f);
     const float total = lanes_sum<W>(u);
     u = total == 0.f ? 0.f : u / total;
   }

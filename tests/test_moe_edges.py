@@ -28,6 +28,30 @@ LOW = [(3, 8, 2), (300, 8, 2), (300, 40, 6), (40, 200, 8)]
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", LOW)
+def test_sigmoids_below_the_least_of_fp32(T, E, k):
+    """Scores whose exponentials overflow have their ratio."""
+    g = torch.Generator().manual_seed(T + E)
+    logits = -90 - 4 * torch.rand(T, E, generator=g) - 100 * (torch.arange(T)[:, None] % 5)
+    logits[1, 1:] = -torch.inf  # one score alone
+    o = dict(score="sigmoid", scale=1.5)
+    r = call(logits, k, o)
+    ids = chosen(logits, k)[0]  # the logits' order
+    assert torch.equal(r.ids.cpu(), ids)
+    p = shares(logits, ids)
+    p[1] = torch.eye(k)[0]
+    assert ((r.weights.cpu().double() - 1.5 * p).abs() <= 64 * U * 1.5 * p).all()
+    dw = torch.randn(T, k, generator=g)
+    got = moe.route_backward(dw.cuda(), logits.cuda(), r).cpu().double()
+    d, grad = 1.5 * dw.double(), torch.zeros(T, E, dtype=torch.float64)
+    bound = torch.zeros_like(grad)
+    mean, mag = (d * p).sum(1, keepdim=True), (d.abs() * p).sum(1, keepdim=True)
+    grad.scatter_(1, ids.long(), p * (d - mean))
+    bound.scatter_(1, ids.long(), 96 * U * p * (d.abs() + mag))
+    assert ((got - grad).abs() <= bound + 1e-38).all()
+
+
+@pytest.mark.gpu
 def test_the_places_of_a_padded_batch_are_indices():
     """x[pairs // k], as the module's documentation has it, with masked tokens."""
     taken = torch.full((1 << 20,), 1 << 30, dtype=I32, device="cuda")
