@@ -52,6 +52,35 @@ def test_sigmoids_below_the_least_of_fp32(T, E, k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", LOW)
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_gradient_of_saturated_sigmoids(T, E, k, renormalize):
+    """The complement of a score near 1 is not what is left of it in fp32."""
+    g = torch.Generator().manual_seed(T)
+    logits = torch.tensor([8.0, -8, 10, 12, -10, 15, 17, 20, -20, 25, 30, 0])[torch.randint(0, 12, (T, E), generator=g)]
+    logits += 0.5 * torch.rand(T, E, generator=g)
+    logits[0] = 15 + torch.arange(E) / 64
+    scale = 1.0 if renormalize else 2.5
+    r = call(logits, k, dict(score="sigmoid", renormalize=renormalize, scale=scale))
+    ids = r.ids.cpu().long()
+    # the logits' order, which float64 no longer sees in scores this near 1
+    assert torch.equal(ids, torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :k])
+    dw = torch.randn(T, k, generator=g)
+    got = moe.route_backward(dw.cuda(), logits.cuda(), r).cpu().double()
+    l, d = logits.double().gather(1, ids), scale * dw.double()
+    rest = torch.sigmoid(-l)
+    if renormalize:
+        p = shares(logits, ids)
+        want, mag = p * (d - (d * p).sum(1, keepdim=True)) * rest, p * (d.abs() + (d.abs() * p).sum(1, keepdim=True)) * rest
+    else:
+        want = d * torch.sigmoid(l) * rest
+        mag = want.abs()
+    grad = torch.zeros(T, E, dtype=torch.float64).scatter_(1, ids, want)
+    bound = torch.zeros(T, E, dtype=torch.float64).scatter_(1, ids, 96 * U * mag)
+    assert ((got - grad).abs() <= bound + 1e-38).all()
+
+
+@pytest.mark.gpu
 def test_the_places_of_a_padded_batch_are_indices():
     """x[pairs // k], as the module's documentation has it, with masked tokens."""
     taken = torch.full((1 << 20,), 1 << 30, dtype=I32, device="cuda")
