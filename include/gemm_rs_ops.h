@@ -228,8 +228,9 @@ int gemm_rs_fp8_status(const void* workspace, void* stream);
  * ids do not depend on rounding: values that fp32 cannot tell apart are compared in
  * 64 bits.  Without a bias experts of a group are compared by their logits.  A token
  * whose mask byte is 0 (mask [T] or NULL) gets ids -1 and weights 0.  A logit of
- * -inf has the score 0; weights are 0 where every chosen score is.  A NaN counts
- * as the lowest logit for the choice, and makes the token's weights NaN.
+ * -inf has the score 0; weights are 0 where every chosen score is.  Logits of +inf
+ * share a softmax equally and leave nothing to the others.  A NaN counts as the lowest
+ * logit, of score 0, for the choice, and makes the token's weights and gradient NaN.
  *
  * The token-expert pairs (pair t * top_k + j) are put in the order of their
  * experts, then of the pairs: rows [T][top_k] is each pair's place (-1 without an

@@ -112,12 +112,19 @@ __device__ __forceinline__ float sigmoid_over(float x, float top) {
   return top == -INFINITY ? 0.f : expf(x - fminf(top, 0.f)) / (1.f + expf(x));
 }
 
-// Scores of a token from its logits (E of them, slots behind E hold -inf).
+// e^(x - top) for top no less than x; infinities that are the largest are equal.
+template <typename F>
+__device__ __forceinline__ F exp_below(F x, F top) {
+  return x == top ? F(1) : exp_of(x - top);
+}
+
+// Scores of a token from its logits (E of them, slots behind E hold -inf).  A NaN counts as -inf; of logits
+// of +inf each takes the same share of a softmax, and the others nothing.
 template <int W, typename F, int kPer>
 __device__ __forceinline__ void scores_of(const float (&logit)[kPer], bool sigmoid, F (&score)[kPer]) {
   if (sigmoid) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) score[i] = F(1) / (F(1) + exp_of(-(F)logit[i]));
+    for (int i = 0; i < kPer; ++i) score[i] = logit[i] != logit[i] ? F(0) : F(1) / (F(1) + exp_of(-(F)logit[i]));
     return;
   }
   float top = -INFINITY;
@@ -127,7 +134,7 @@ __device__ __forceinline__ void scores_of(const float (&logit)[kPer], bool sigmo
   F sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    score[i] = top == -INFINITY ? F(0) : exp_of((F)logit[i] - (F)top);
+    score[i] = top == -INFINITY || logit[i] != logit[i] ? F(0) : exp_below((F)logit[i], (F)top);
     sum += score[i];
   }
   sum = lanes_sum<W>(sum);
@@ -322,7 +329,7 @@ __device__ __forceinline__ void route_tokens(const RouteParams& p, int t0, int l
   const bool in = sub < p.top_k;
   if (p.sigmoid || p.renormalize) {
     const float top = p.renormalize ? lanes_max<W>(in ? mine : -INFINITY) : 0.f;
-    mine = p.sigmoid ? sigmoid_over(mine, top) : top == -INFINITY ? 0.f : expf(mine - top);
+    mine = p.sigmoid ? sigmoid_over(mine, top) : top == -INFINITY ? 0.f : exp_below(mine, top);
   }
   float total = 1.f;
   if (p.renormalize) {
@@ -727,6 +734,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
     const int e = sub + W * i;
     logit[i] = e < p.E ? load_logit(p.logits, p.bf16, (long long)t * p.E + e) : -INFINITY;
   }
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) nan |= logit[i] != logit[i];
   int id = -1;
   float g = 0.f;
   if (sub < p.top_k) {
@@ -735,6 +745,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
   }
   if (!p.sigmoid && !p.renormalize) scores_of<W>(logit, false, score);
   const bool has = (unsigned)id < (unsigned)p.E;
+  nan = lanes_ballot<W>(nan, lane) != 0;
+  nan = lanes_ballot<W>(has, lane) != 0 && nan;  // masked tokens have no gradient
   // the chosen one's score in a softmax of all, else its logit
   const bool dense = !p.sigmoid && !p.renormalize;  // every expert has a gradient
 #pragma unroll
@@ -749,7 +761,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
   }
   if (p.renormalize) {
     const float top = lanes_max<W>(s);
-    u = top == -INFINITY || !has ? 0.f : p.sigmoid ? sigmoid_over(s, top) : expf(s - top);
+    u = top == -INFINITY || !has ? 0.f : p.sigmoid ? sigmoid_over(s, top) : exp_below(s, top);
     const float total = lanes_sum<W>(u);
     u = total == 0.f ? 0.f : u / total;
   }
@@ -766,7 +778,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_backward_kernel(const 
     const int e = sub + W * i;
     if (e >= p.E) continue;
     const long long at = (long long)t * p.E + e;
-    const float grad = values[e];
+    const float grad = nan ? __uint_as_float(0x7FC00000u) : values[e];
     if (p.bf16)
       static_cast<uint16_t*>(p.dlogits)[at] = (uint16_t)pack_bf16x2(grad, 0.f);
     else

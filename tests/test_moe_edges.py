@@ -24,6 +24,15 @@ def shares(logits, ids):
     return torch.softmax(-torch.nn.functional.softplus(-l), 1)
 
 
+def by_logits(logits, p, k, groups, top_groups):
+    best = p.unflatten(1, (groups, -1)).sort(-1, descending=True).values[..., :2].sum(-1)
+    kept = torch.sort(best, dim=-1, descending=True, stable=True).indices[:, :top_groups]
+    stays = torch.zeros_like(best, dtype=torch.bool).scatter_(1, kept, True).repeat_interleave(logits.shape[1] // groups, 1)
+    left = torch.where(stays, logits.double(), -1e300)  # below every logit here but a NaN's -inf
+    left = torch.where(stays & torch.isneginf(logits), -1e299, left)
+    return torch.sort(left, dim=1, descending=True, stable=True).indices[:, :k].int()
+
+
 LOW = [(3, 8, 2), (300, 8, 2), (300, 40, 6), (40, 200, 8)]
 
 
@@ -78,6 +87,57 @@ def test_gradient_of_saturated_sigmoids(T, E, k, renormalize):
     grad = torch.zeros(T, E, dtype=torch.float64).scatter_(1, ids, want)
     bound = torch.zeros(T, E, dtype=torch.float64).scatter_(1, ids, 96 * U * mag)
     assert ((got - grad).abs() <= bound + 1e-38).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E", [(8, 40), (300, 40), (300, 200), (40, 200)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_choice_beside_logits_that_are_not_finite(T, E, score):
+    """A NaN counts as the lowest logit, +inf takes a softmax whole; neither touches the order of the others."""
+    g = torch.Generator().manual_seed(T + E)
+    logits, bias = torch.randn(T, E, generator=g), 0.2 * torch.randn(E, generator=g)
+    logits[0, E - 1] = torch.nan
+    logits[1, E - 1] = torch.inf
+    logits[2, [0, E - 2]] = torch.inf
+    logits[3, [E - 3, 5]] = torch.nan
+    logits[4, [3, E - 4]] = torch.tensor([torch.nan, torch.inf])
+    clean = torch.where(logits.isnan(), -torch.inf, logits)
+    top = clean.max(1, keepdim=True).values
+    # scores as the definition's limit, for the oracle: of 2000 in place of an infinity the rest's are 0
+    finite = torch.where(torch.isposinf(clean), 2000.0, clean) if score == "softmax" else clean
+    k = 4
+    for o in (dict(groups=5, top_groups=2), dict(groups=4, top_groups=1), dict(bias=bias), dict(groups=5, top_groups=2, bias=bias)):
+        for renormalize in (True, False):
+            opts = {n: v for n, v in o.items() if n != "bias"}
+            r = call(logits, k, dict(opts, score=score, renormalize=renormalize), o.get("bias"))
+            ids, p = chosen(finite, k, o.get("bias"), score, opts.get("groups", 1), opts.get("top_groups"))
+            if "bias" not in o:  # then experts of the groups that stay are compared by their logits
+                ids = by_logits(clean, p, k, **opts)
+            assert torch.equal(r.ids.cpu(), ids)
+            w = r.weights.cpu()
+            nan = logits.isnan().any(1)
+            assert w[nan].isnan().all()
+            rest = torch.where(ids >= 0, p.gather(1, ids.long()), 0)
+            want = rest / rest.sum(1, keepdim=True) if renormalize else rest
+            assert ((w.double() - want).abs() <= (64 + 16) * U * want + 1e-38)[~nan].all()
+            d = moe.route_backward(torch.ones(T, k).cuda(), logits.cuda(), r).cpu()
+            assert d[nan].isnan().all() and d[~nan].isfinite().all()
+    assert top[1] == torch.inf
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(6, 8, 2), (300, 40, 6), (40, 200, 3)])
+def test_masked_tokens_of_any_logits_have_no_gradient(T, E, k):
+    logits = torch.randn(T, E, generator=torch.Generator().manual_seed(T))
+    for t, v in enumerate((torch.nan, torch.inf, -torch.inf)):
+        logits[t, 1] = v
+    logits[3] = torch.nan
+    mask = torch.arange(T) > 3
+    for o in (dict(), dict(renormalize=False), dict(score="sigmoid"), dict(score="sigmoid", renormalize=False)):
+        r = call(logits, k, o, mask=mask)
+        assert (r.ids[:4] == -1).all() and (r.weights[:4] == 0).all()
+        d = moe.route_backward(torch.ones(T, k).cuda(), logits.cuda(), r).cpu()
+        assert (d[:4] == 0).all() and d.isfinite().all()
 
 
 @pytest.mark.gpu
