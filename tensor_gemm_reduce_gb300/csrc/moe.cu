@@ -233,9 +233,9 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&logit
   const bool check = kCheck && p.bias;
   const int picks = check ? p.top_k + 1 : p.top_k;
   int found = -1;
-  for (int j = 0; j < picks; ++j) {
-    Key best = key[0];
-    int e = sub;
+  auto next = [&](Key& best, int& e) {  // the best of those that are left
+    best = key[0];
+    e = sub;
 #pragma unroll
     for (int i = 1; i < kPer; ++i)
       if (key[i] > best) {
@@ -243,10 +243,15 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&logit
         e = sub + W * i;
       }
     lanes_best<W>(best, e);
-    if (j == sub && best != 0) found = e;  // 0: only behind the last of the experts that there are
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (e == sub + W * i) key[i] = 0;
+  };
+  Key best;
+  int e;
+  for (int j = 0; j < picks; ++j) {
+    next(best, e);
+    if (j == sub && best != 0) found = e;  // 0: only behind the last of the experts that there are
   }
   if (check) {  // is one nearer to the one before than the errors, and not its equal?
     float v = 0.f, l = 0.f, b = 0.f;
@@ -260,7 +265,17 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&logit
     __syncwarp();
     if (found >= 0) l = logits[found];
     const float pv = __shfl_up_sync(kAll, v, 1, W), pl = __shfl_up_sync(kAll, l, 1, W), pb = __shfl_up_sync(kAll, b, 1, W);
-    if (lanes_ballot<W>(sub > 0 && found >= 0 && near_values(v, pv, slack) && !(l == pl && b == pb), lane)) sure = false;
+    const bool same = l == pl && b == pb;
+    if (lanes_ballot<W>(sub > 0 && found >= 0 && near_values(v, pv, slack) && !same, lane)) sure = false;
+    // where the last that is chosen and the first that is not are equals, the first behind them that is none
+    bool equals = (lanes_ballot<W>(found >= 0 && same, lane) >> p.top_k) & 1u;
+    const float lv = __shfl_sync(kAll, v, p.top_k, W), ll = __shfl_sync(kAll, l, p.top_k, W), lb = __shfl_sync(kAll, b, p.top_k, W);
+    while (__any_sync(kAll, equals)) {
+      next(best, e);
+      if (!equals) continue;
+      equals = best != 0 && logits[e] == ll && load_f32(p.bias + e) == lb;
+      if (best != 0 && !equals && near_values((float)values[e], lv, slack)) sure = false;
+    }
   }
   *id = found >= 0 ? found : 0;
   return sure;

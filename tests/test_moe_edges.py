@@ -126,6 +126,24 @@ def test_a_choice_beside_logits_that_are_not_finite(T, E, score):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,E", [(3, 12), (300, 12), (300, 96), (300, 200), (30, 200)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_equal_choices_at_the_border_hide_no_better_one(T, E, score):
+    """The last that is chosen and the first that is not are equal, and a third is above both by less than fp32 tells."""
+    g = torch.Generator().manual_seed(E)
+    bias = torch.ones(E)
+    logits = torch.randint(-22, -18, (T, E), generator=g).float()
+    logits[:, 0] = 0
+    logits[0] = torch.full((E,), -40.0)
+    logits[0, :4] = torch.tensor([0.0, -20, -20, -19])
+    for k in (2, 3, 7):
+        ids, _ = chosen(logits, k, bias, score)
+        if T > 3:
+            assert (ids[:, 1] != 1).any()
+        assert torch.equal(call(logits, k, dict(score=score), bias).ids.cpu(), ids)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,E,k", [(6, 8, 2), (300, 40, 6), (40, 200, 3)])
 def test_masked_tokens_of_any_logits_have_no_gradient(T, E, k):
     logits = torch.randn(T, E, generator=torch.Generator().manual_seed(T))
