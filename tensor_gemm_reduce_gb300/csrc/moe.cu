@@ -142,9 +142,12 @@ __device__ __forceinline__ void scores_of(const float (&logit)[kPer], bool sigmo
   for (int i = 0; i < kPer; ++i) score[i] = top == -INFINITY ? F(0) : score[i] / sum;
 }
 
-// A choice is a score plus a bias.  A softmax score is off by at most 23 times 2^-24 of the token's
-// largest score (exponential 2, its argument 1, a sum over slots and lanes 18, quotient 2), a sigmoid
-// by 5 times 2^-24 (exponential 2, sum 1, quotient 2), the choice by another 2^-24 of itself.  `slack` is
+// A choice is a score plus a bias.  In units of 2^-24, a softmax score is off by at most 32 of the
+// token's largest score: its exponential by 4 (two units in the last place) and by 1 for its argument x
+// (|x| e^x is at most 1/e), the sum by the 4 of its terms' exponentials, by 3.4 for their arguments (the mean of
+// |x| weighted by e^x, of 255 experts beside the largest, is below that) and by 18 for adding up slots
+// and lanes, the quotient by 1; a sigmoid s by 5 (4 s (1 - s) for its exponential, sum 1, quotient 1, the
+// rest to spare); the choice by another 1 of itself.  `slack` is
 // twice the multiple for the score.  With a quarter more for the bound's own roundings, two choices may
 // be in the wrong order where they are this near.  (A bound for scores of 1 sent 20 to 30 times as many
 // tokens of 96 experts to 64 bits.)
@@ -171,7 +174,7 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&logit
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) top = fmaxf(top, choice[i]);
-      slack = p.sigmoid ? 2 * 5.f : 2 * 23.f * lanes_max<W>(top);
+      slack = p.sigmoid ? 2 * 5.f : 2 * 32.f * lanes_max<W>(top);
     }
     if (p.bias)
 #pragma unroll

@@ -144,6 +144,20 @@ def test_equal_choices_at_the_border_hide_no_better_one(T, E, score):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("E", [40, 96, 128, 200, 256])
+def test_nearly_equal_softmax_scores_of_many_experts(E):
+    """Biases that make up for one token's scores up to their rounding; the others' logits are a little off it."""
+    g = torch.Generator().manual_seed(E)
+    base = torch.randn(1, E, generator=g)
+    bias = (0.3 - chosen(base, 1)[1][0]).float()
+    for spread in (1e-7, 3e-6, 3e-5):
+        logits = base + spread * torch.randn(600, E, generator=g)
+        for T in (600, 20):
+            ids, _ = chosen(logits[:T], 6, bias)
+            assert torch.equal(call(logits[:T].contiguous(), 6, {}, bias).ids.cpu(), ids)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,E,k", [(6, 8, 2), (300, 40, 6), (40, 200, 3)])
 def test_masked_tokens_of_any_logits_have_no_gradient(T, E, k):
     logits = torch.randn(T, E, generator=torch.Generator().manual_seed(T))
