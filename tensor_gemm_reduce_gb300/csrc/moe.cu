@@ -884,6 +884,23 @@ __global__ void __launch_bounds__(kCombineThreads) weight_grad_kernel(const DotP
   if (lane == 0) p.dweights[pair] = total;
 }
 
+// dA of an empty contraction: zero for the rows that belong to an expert.
+struct ClearParams {
+  uint4* out;
+  const int* offsets;
+  int experts, pairs, vec;  // vectors of 8 in a row
+  long long total;
+};
+
+__global__ void __launch_bounds__(kCombineThreads) clear_rows_kernel(const ClearParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int used = expert_row(p.offsets, p.experts, p.pairs);
+  const long long stride = (long long)gridDim.x * kCombineThreads;
+  for (long long i = (long long)blockIdx.x * kCombineThreads + threadIdx.x; i < p.total; i += stride)
+    if ((int)(i / p.vec % p.pairs) < used) st_global_v4(p.out + i, make_uint4(0, 0, 0, 0));
+}
+
 int check_route(const gemm_rs_route_desc* d) {
   if (!d) return GEMM_RS_ERR_INVALID_ARG;
   if (d->T < 0 || d->E < 1 || d->E > kMaxExperts || d->top_k < 1 || d->top_k > kMaxTopK || d->top_k > d->E ||
@@ -1231,11 +1248,25 @@ int backward(Fp8Scale scale, const gemm_rs_moe_desc* d, const void* dout, const 
   if (!workspace) return GEMM_RS_ERR_WORKSPACE;
   const int64_t P = d->T * d->top_k;
   if (P == 0 || d->N == 0 || d->K == 0) {
+    const bool some_dA = dA && P > 0 && d->K > 0;
+    if (some_dA && !offsets) return GEMM_RS_ERR_INVALID_ARG;
     rc = clear(workspace, sizeof(uint32_t), st);
-    if (!rc && dA) rc = clear(dA, (size_t)P * d->K * 2, st);
     if (!rc && dW) rc = clear(dW, (size_t)d->E * d->K * d->N * 2, st);
     if (!rc && dweights) rc = clear(dweights, (size_t)P * 4, st);
-    return rc;
+    if (rc || !some_dA) return rc;
+    int sms = 0;
+    rc = current_device_sms(&sms);
+    if (rc) return rc;
+    ClearParams c;
+    c.out = static_cast<uint4*>(dA);
+    c.offsets = static_cast<const int*>(offsets);
+    c.experts = (int)d->E;
+    c.pairs = (int)P;
+    c.vec = (int)(d->K / kWorld / 8);
+    c.total = P * (d->K / 8);
+    const long long blocks = (c.total + kCombineThreads - 1) / kCombineThreads;
+    return launch_overlapped(clear_rows_kernel, dim3((unsigned)(blocks < 16ll * sms ? blocks : 16ll * sms)), kCombineThreads, 0,
+                             st, c);
   }
   if (!dA && !dW && !dweights) return clear(workspace, sizeof(uint32_t), st);
   if (!dout || !weights || !rows || !pairs || !offsets || (dA && (!codes || !scales)) ||

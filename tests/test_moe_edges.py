@@ -173,6 +173,25 @@ def test_masked_tokens_of_any_logits_have_no_gradient(T, E, k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 200])
+def test_an_empty_contraction_leaves_the_rows_behind_the_last(T):
+    E, k, K = 4, 2, 512
+    ids = torch.randint(0, E, (T, k), generator=torch.Generator().manual_seed(T), dtype=I32)
+    ids[::3] = -1
+    r = moe.arrange(ids.cuda(), torch.ones(T, k).cuda(), E)
+    used = int(r.offsets[-1])
+    assert 0 < used < T * k
+    weight = fp8.quantize(torch.empty(E, 8, K // 8, 0, dtype=BF16, device="cuda"))
+    ck, ws = moe.Checkpoint(r, weight), moe.new_workspace(r, weight)
+    moe.forward(torch.zeros(8, T * k, K // 8, dtype=BF16, device="cuda"), weight, r, checkpoint=ck)
+    dA = torch.full((8, T * k, K // 8), 3.0, dtype=BF16, device="cuda")
+    dw = torch.full((T, k), 3.0, device="cuda")
+    moe.backward(torch.empty(T, 0, dtype=BF16, device="cuda"), weight, r, ck, out=(dA, None, dw), workspace=ws)
+    assert fp8.status(ws) == G.GEMM_RS_OK
+    assert (dA[:, :used] == 0).all() and (dA[:, used:] == 3).all() and (dw == 0).all()
+
+
+@pytest.mark.gpu
 def test_the_places_of_a_padded_batch_are_indices():
     """x[pairs // k], as the module's documentation has it, with masked tokens."""
     taken = torch.full((1 << 20,), 1 << 30, dtype=I32, device="cuda")
