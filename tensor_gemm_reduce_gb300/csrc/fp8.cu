@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, kGather ? 2 : kTokens ? 3 : 4) quant
       const int row = row0 + ty + 16 * i, pair = p.pairs[row < end ? row : row0];
       const bool valid = row < end && (unsigned)pair < (unsigned)p.M;
       weight[i] = valid ? p.weights[pair] : 0.f;
-      source[i] = valid ? pair / p.top_k : 0;
+      source[i] = valid ? pair / p.top_k : -1;
     }
   }
   const int cb1 = kGather && cb0 + p.span < p.cb ? cb0 + p.span : kGather ? p.cb : cb0 + 1;
@@ -195,10 +195,11 @@ __global__ void __launch_bounds__(kThreads, kGather ? 2 : kTokens ? 3 : 4) quant
       const int row = row0 + ty + 16 * i;
       raw[i] = make_uint4(0, 0, 0, 0);
       if (row < end && in) {
-        if constexpr (kGather)
-          raw[i] = load_v4(p.x + (long long)source[i] * p.vec + col);  // top_k rows read it
-        else
+        if constexpr (kGather) {
+          if (source[i] >= 0) raw[i] = load_v4(p.x + (long long)source[i] * p.vec + col);  // top_k rows read it
+        } else {
           raw[i] = load_v4_stream(p.x + plane * p.x_plane + (long long)row * p.vec + col);
+        }
       }
     }
     if constexpr (kGather) {

@@ -192,6 +192,23 @@ def test_an_empty_contraction_leaves_the_rows_behind_the_last(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [6, 150])
+@pytest.mark.parametrize("scales", [torch.float32, torch.float8_e8m0fnu])
+def test_a_pair_outside_the_tensors_takes_nothing_of_the_first_token(T, scales):
+    E, k, N, K = 3, 2, 136, 1088
+    ids, w, A, W, dout = experts(T, E, k, N, K, False)
+    ids[0] = -1  # a padded token, whose gradient is anything
+    dout[0] = torch.nan
+    weight, r = fp8.quantize(W.cuda(), scales=scales), moe.arrange(ids.cuda(), w.cuda(), E)
+    ck = moe.Checkpoint(r, weight)
+    moe.forward(A.cuda(), weight, r, checkpoint=ck)
+    used = int(r.offsets[-1])
+    r.pairs[3] = 1 << 30
+    dA, dW, _ = moe.backward(dout.cuda(), weight, r, ck)
+    assert not dA[:, 3].any() and dA[:, :used].isfinite().all() and dW.isfinite().all()
+
+
+@pytest.mark.gpu
 def test_the_places_of_a_padded_batch_are_indices():
     """x[pairs // k], as the module's documentation has it, with masked tokens."""
     taken = torch.full((1 << 20,), 1 << 30, dtype=I32, device="cuda")
