@@ -209,6 +209,20 @@ def test_a_pair_outside_the_tensors_takes_nothing_of_the_first_token(T, scales):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(65536, 96, 6), (45000, 128, 7), (34001, 256, 8), (40000, 33, 8), (70001, 70, 4),
+                                   (49999, 32, 7)])
+def test_many_pairs_of_many_experts(T, E, k):
+    """More than 262144 pairs and 32 experts or more: each number of CTAs that share an expert's ids."""
+    ids = torch.randint(-1, E + 1, (T, k), generator=torch.Generator().manual_seed(T), dtype=I32)
+    ids[T // 3:T // 2] = 5  # many of one
+    r = moe.Routing(T, k, E)
+    r.pairs.fill_(-7)
+    moe.arrange(ids.cuda(), torch.rand(T, k).cuda(), E, out=r)
+    assert_arranged(r, ids)
+    assert (r.pairs[int(r.offsets[-1]):] == -7).all()
+
+
+@pytest.mark.gpu
 def test_the_places_of_a_padded_batch_are_indices():
     """x[pairs // k], as the module's documentation has it, with masked tokens."""
     taken = torch.full((1 << 20,), 1 << 30, dtype=I32, device="cuda")
@@ -230,3 +244,12 @@ def test_a_new_routing_holds_places_of_the_tensors(monkeypatch):
     monkeypatch.setattr(torch, "empty", lambda *s, **kw: empty(*s, **kw).fill_(1 << 20))
     r = moe.Routing(5, 2, 4, device="cpu")
     assert ((r.pairs >= 0) & (r.pairs < 10)).all()
+
+
+@pytest.mark.parametrize("scales", [torch.float32, torch.float8_e8m0fnu])
+@pytest.mark.parametrize("N,K,experts", [(0, 512, None), (0, 512, 3), (16, 0, None), (0, 0, 2)])
+def test_loading_a_weight_of_nothing(N, K, experts, scales):
+    weight = fp8.Weight(N, K, experts, device="cpu", scales=scales)
+    codes = torch.zeros(weight.shape).to(torch.float8_e4m3fn)
+    assert weight.load(codes, torch.zeros(weight.scales.shape).to(scales)) is weight
+    assert weight.codes.shape == weight.shape
