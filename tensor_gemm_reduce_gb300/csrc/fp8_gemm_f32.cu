@@ -9,10 +9,16 @@
 // two accumulators in TMEM, and while the next step is multiplied eight warps of each CTA read it,
 // scale it and add it to sums in fp32, rounded to nearest, that stay in their registers: 128
 // of a thread's 216, which the other four warps give up with setmaxnreg.
-// Scales go through a ring in shared memory, a slot for each step: for weights a row's scale
+// Scales go through two slots in shared memory, of four steps each: for weights a row's scale
 // times its columns', for dW rows' and columns' apart.
 // Warps in each CTA: 0 loads A, 2 loads B, 3 brings scales, 1 issues the MMAs (first
 // CTA of the pair), 4 to 11 scale, sum and store.
+// Bound by the additions, and by a step's way from MMA to sums and back, which two accumulators do not hide
+// whole: an accumulator is handed back as soon as its last columns are in registers, before they are added
+// (in that order 2048 x 8192 x 8192 forward took 158 us in place of 190, with every part added before the
+// next is read 198).
+#include <type_traits>
+
 #include "fp8_tiles.cuh"
 
 using namespace grs;
@@ -20,8 +26,9 @@ using namespace grs::tiles;
 
 namespace {
 
-constexpr int kSlots = 8;                 // of scales
-constexpr int kSlotBytes = 384 * 4;       // 128 rows' for each half of the columns; dW: 128 rows' and 256 columns'
+constexpr int kSlots = 2, kPerSlot = 4;   // of scales, and steps in a slot, counted from a tile's first
+constexpr int kStepBytes = 384 * 4;       // 128 rows' for each half of the columns; dW: 128 rows' and 256 columns'
+constexpr int kSlotBytes = kPerSlot * kStepBytes;
 constexpr int kSmemBuf = kSmemScales + kSlots * kSlotBytes;
 constexpr int kSmemBar = kSmemBuf + kEpiWarps * kBufBytes;
 constexpr int kNumBars = 2 * kStages + 2 * kSlots + 5;  // full, empty, sf_full, sf_empty, acc_full[2], acc_empty[2], drain
@@ -60,10 +67,21 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// sums[0..15] += scaled v[0..31]: by one factor, or by the row's and the columns' own.
+// sums[0..15] += scaled v[0..31]: by one factor, or by the row's and the columns' own.  Packed additions run on
+// one of the two pipes that single ones share, so every third pair is added by single ones: 2048 x 8192 x 8192
+// forward 156 us with packed ones alone, 142 with a quarter single, 140 with a third, 165 with half.
 __device__ __forceinline__ void add_scaled(uint64_t* sums, const uint32_t (&v)[32], uint64_t factor) {
+  const float f = __uint_as_float((uint32_t)factor);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) sums[i] = fma2(pack2(v[2 * i], v[2 * i + 1]), factor, sums[i]);
+  for (int i = 0; i < 16; ++i) {
+    if (i % 3 != 2) {
+      sums[i] = fma2(pack2(v[2 * i], v[2 * i + 1]), factor, sums[i]);
+    } else {
+      const float x = fmaf(__uint_as_float(v[2 * i]), f, __uint_as_float((uint32_t)sums[i]));
+      const float y = fmaf(__uint_as_float(v[2 * i + 1]), f, __uint_as_float((uint32_t)(sums[i] >> 32)));
+      sums[i] = pack2(__float_as_uint(x), __float_as_uint(y));
+    }
+  }
 }
 __device__ __forceinline__ void add_scaled_columns(uint64_t* sums, const uint32_t (&v)[32], uint64_t factor, uint32_t columns) {
 #pragma unroll
@@ -250,41 +268,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else {
       // ------------------------------------------------------------- scales
-      // kBatch steps' are loaded, then written one by one.  dW's steps have three times as many.
-      constexpr int kBatch = kKind == kFp8WeightGrad || kKind == kBothGrads ? 2 : 4;
-      int slot = 0, step = 0, end = 0;
+      // A slot's steps are loaded kBatch at a time; dW's have three times as many words.
+      constexpr int kBatch = kKind == kFp8WeightGrad || kKind == kBothGrads ? 2 : kPerSlot;
+      int slot = 0;
       uint32_t phase = 0;
-      auto fetch = [&](Scales* x) {  // the next step's, of this tile or the next one
-        while (step >= end) {
-          if (!walk.next(&t)) return false;
-          step = t.step0;
-          end = t.step0 + t.steps;
-        }
-        load_scales<kKind>(p, t, cta, lane, step++, x);
-        return true;
-      };
-      Scales sf[kBatch];
-      bool ok = true, more = true;
-      while (ok && more) {
-        int n = 0;
+      bool ok = true;
+      while (ok && walk.next(&t)) {
+        for (int s0 = 0; ok && s0 < t.steps; s0 += kPerSlot) {
+          Scales sf[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if (more) {
-            more = fetch(&sf[j]);
-            n += more;
-          }
+          for (int j0 = 0; j0 < kPerSlot; j0 += kBatch) {
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          if (!ok || j >= n) continue;
-          int got = 0;
-          if (lane == 0) got = wait_bar(bar_sf_empty + 8 * slot, phase ^ 1u, kLimitNs, cta_abort) ? 1 : 0;
-          got = __shfl_sync(0xffffffffu, got, 0);
-          if (!got) {
-            if (lane == 0) give_up(abort_addr);
-            ok = false;
-            continue;
+            for (int j = 0; j < kBatch; ++j)
+              if (s0 + j0 + j < t.steps) load_scales<kKind>(p, t, cta, lane, t.step0 + s0 + j0 + j, &sf[j]);
+            if (j0 == 0) {
+              int got = 0;
+              if (lane == 0) got = wait_bar(bar_sf_empty + 8 * slot, phase ^ 1u, kLimitNs, cta_abort) ? 1 : 0;
+              got = __shfl_sync(0xffffffffu, got, 0);
+              if (!got) {
+                if (lane == 0) give_up(abort_addr);
+                ok = false;
+                break;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+              if (s0 + j0 + j < t.steps)
+                store_scales<kKind>(sbase + kSmemScales + slot * kSlotBytes + (j0 + j) * kStepBytes, lane, sf[j]);
           }
-          store_scales<kKind>(sbase + kSmemScales + slot * kSlotBytes, lane, sf[j]);
+          if (!ok) break;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_sf_full + 8 * slot);
           if (++slot == kSlots) {
@@ -301,62 +313,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // Lane = row of the warp's 32, 128 of the tile's columns.
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t buf = sbase + kSmemBuf + (uint32_t)(warp - 4) * kBufBytes;
-    int acc = 0, slot = 0;
-    uint32_t acc_phase = 0, sf_phase = 0;
+    const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
+    uint32_t n = 0, m = 0;  // steps and slots so far: sums n & 1 in TMEM, slot m & 1
     bool ok = true;
-    while (ok && walk.next(&t)) {
+    for (int at = pair;; at += pairs) {
+      // what the steps do not need of the tile is looked up again behind them: registers
+      if (!Walk<kKind>(p, start, blocks, at, pairs).next(&t)) break;
       uint64_t sums[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) sums[i] = 0;
-      const bool columns = kind_of<kKind>(t) == kFp8WeightGrad;
-      for (int s = 0; s < t.steps; ++s) {
-        int got = 0;
-        if (lane == 0)
-          got = wait_bar(bar_sf_full + 8 * slot, sf_phase, kLimitNs, cta_abort) &&
-                wait_bar(bar_acc_full + 8 * acc, acc_phase, kLimitNs, cta_abort);
-        got = __shfl_sync(0xffffffffu, got, 0);
-        if (!got) {
-          if (lane == 0) give_up(abort_addr);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile + half * 128);
-        const uint32_t scales = sbase + kSmemScales + slot * kSlotBytes;
+      auto add_steps = [&](auto columns, const int steps) {  // whether columns have scales of their own
+        constexpr bool kColumns = decltype(columns)::value;
         uint32_t v[2][32];
-        tmem_ld_32x32b_x32(taddr, v[0]);
-        const uint32_t own = ld_shared_u32(scales + 4 * ((columns ? 0 : half * 128) + q * 32 + lane));
-        const uint64_t factor = pack2(own, own);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {  // one part is read while the one before is added
-          tmem_ld_wait(v[c & 1]);
-          if (c < 3) {
-            tmem_ld_32x32b_x32(taddr + 32 * (c + 1), v[(c + 1) & 1]);
-          } else {  // all read: back to the MMA warp
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (cta == 0)
-                mbar_arrive(bar_acc_empty + 8 * acc);
-              else
-                mbar_arrive_remote(mapa_shared(bar_acc_empty + 8 * acc, 0));
-            }
+        uint64_t factor = 0;
+        uint32_t scales = 0;
+        // Waits for step s's products and scales.
+        auto begin = [&](int s) {
+          const bool got = (s % kPerSlot != 0 || wait_bar(bar_sf_full + 8 * (m & 1), (m >> 1) & 1, kLimitNs, cta_abort)) &&
+                           wait_bar(bar_acc_full + 8 * (n & 1), (n >> 1) & 1, kLimitNs, cta_abort);
+          if (!__all_sync(0xffffffffu, got)) {
+            if (lane == 0) give_up(abort_addr);
+            return false;
           }
-          if (columns)
+          tc_fence_after();
+          scales = sbase + kSmemScales + (m & 1) * kSlotBytes + (uint32_t)(s % kPerSlot) * kStepBytes;
+          const uint32_t own = ld_shared_u32(scales + 4 * ((kColumns ? 0 : half * 128) + q * 32 + lane));
+          factor = pack2(own, own);
+          return true;
+        };
+        auto ask = [&](int c) { tmem_ld_32x32b_x32(tbase + (n & 1) * kTile + 32 * c, v[c & 1]); };
+        auto add = [&](int c) {
+          if constexpr (kColumns)
             add_scaled_columns(sums + 16 * c, v[c & 1], factor, scales + 4 * (128 + half * 128 + 32 * c));
           else
             add_scaled(sums + 16 * c, v[c & 1], factor);
+        };
+        for (int s = 0; s < steps; ++s) {
+          ok = begin(s);
+          if (!ok) return;
+          // two parts of 32 columns are on their way or being added at a time
+          ask(0);
+          ask(1);
+          tmem_ld_wait(v[0]);
+          tmem_ld_wait(v[1]);
+          add(0);
+          ask(2);
+          add(1);
+          ask(3);
+          tmem_ld_wait(v[0]);
+          tmem_ld_wait(v[1]);
+          tc_fence_before();  // all read: back to the MMA warp
+          __syncwarp();
+          if (lane == 0) {
+            if (cta == 0)
+              mbar_arrive(bar_acc_empty + 8 * (n & 1));
+            else
+              mbar_arrive_remote(mapa_shared(bar_acc_empty + 8 * (n & 1), 0));
+          }
+          ++n;
+          add(2);
+          add(3);
+          if (s % kPerSlot == kPerSlot - 1 || s == steps - 1) {  // the slot's scales have been read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_sf_empty + 8 * (m & 1));
+            ++m;
+          }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_sf_empty + 8 * slot);
-        if (++slot == kSlots) {
-          slot = 0;
-          sf_phase ^= 1u;
-        }
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+      };
+      if (t.steps > 0) {
+        if (kind_of<kKind>(t) == kFp8WeightGrad)
+          add_steps(std::true_type{}, t.steps);
+        else
+          add_steps(std::false_type{}, t.steps);
       }
       if (!ok) break;
+      Walk<kKind>(p, start, blocks, at, pairs).next(&t);
       uint32_t v[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
