@@ -4,7 +4,7 @@
 //
 // Tiles of 256 x 256, one at a time for each pair of CTAs (cta_group::2).  Operands are read as
 // they lie in memory, K-major or MN-major, through TMA.  dA and dW are independent, so a
-// backward pass multiplies both in one launch, dA's tiles first.
+// backward pass may multiply both in one launch, dA's tiles first.
 #pragma once
 #include <cuda.h>
 
