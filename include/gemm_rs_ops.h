@@ -158,7 +158,8 @@ int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int has_zeros, co
  *
  * the codes of a step of 128 inner elements are multiplied and summed on the
  * tensor cores in fp32, scaled by the product of the two scales, and added up
- * in fp32; outputs are rounded to bf16 once.  The same call gives the same bits; with
+ * in fp32 (where the product of two scales is no normal number of fp32, the step loses
+ * bits or is infinite); outputs are rounded to bf16 once.  The same call gives the same bits; with
  * other rows beside it, or for dA without dW, a sum may run in another order.
  *
  * Weights: codes [experts][8][ceil(N/128)][K/8][128] e4m3 (128 columns of W at a
@@ -167,7 +168,7 @@ int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int has_zeros, co
  * well.  experts is 1 for the layer itself.
  *
  * The entries whose names end in _e8m0 are the same in a form that large products
- * take half the time in, for some accuracy: every block's scale, of weights, inputs and
+ * take half to two thirds of the time in, for some accuracy: every block's scale, of weights, inputs and
  * gradients alike, is a power of two, 2^e with the least e >= -126 such that the
  * block's largest magnitude is at most 448 * 2^e; codes are the elements over 2^e,
  * and the tensor cores apply the scales, so that the whole contraction is summed in

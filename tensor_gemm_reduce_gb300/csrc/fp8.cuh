@@ -123,7 +123,7 @@ struct Fp8Few {
 };
 // Whether fp8_few takes less time than fp8_product; with_weight_grad: dA beside which dW is wanted too,
 // which fp8_products would multiply in the same launch.
-bool fp8_few_serves(Fp8Kind kind, Fp8Scale scale, const Fp8Rows& rows, int64_t N, int64_t Kr, bool with_weight_grad, int sms);
+bool fp8_few_serves(Fp8Kind kind, const Fp8Rows& rows, int64_t N, int64_t Kr, bool with_weight_grad, int sms);
 int fp8_few(const Fp8Few& p, cudaStream_t stream);
 
 }  // namespace grs

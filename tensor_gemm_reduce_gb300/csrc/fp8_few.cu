@@ -3,7 +3,10 @@
 //
 // Bound by reading the weights once.  They are the operand with 128 rows: a CTA
 // multiplies 128 columns of W (for dA: 128 rows) by all tokens (16 to 128 columns of the
-// accumulator) on tcgen05 with the scales applied by the tensor cores.  The contraction is cut
+// accumulator) on tcgen05.  Scales that are powers of two are applied by the tensor cores; with fp32 scales each
+// step of 128 goes to sums of its own in TMEM (four in turn), which the warps 4 to 7 scale and add up in
+// their registers, unseen beside the weights' way (1 x 8192 x 28672 40.0 us against 39.9, 24 x 8192 x 8192 17.8
+// against 17.1, 64 x 8192 x 28672 47).  The contraction is cut
 // among the CTAs of a cluster, so that two CTAs on each SM stream weights at the same time
 // (up to 64 rows: their shared memory and TMEM leave room for two); their partial sums meet in
 // distributed shared memory, in the order of the CTAs, and the weighting of a token's experts
@@ -619,11 +622,12 @@ Grid grid_of(Fp8Kind kind, int64_t M, int64_t N, int64_t Kr, int sms) {
 }  // namespace
 
 // Estimated times, in units of 10 ns, fitted to 150 shapes of 1 to 128 rows, 152 to 28672 columns and 1 to 16
-// experts; the choice is within 15% of the faster one.  Here a CTA goes through its part of
+// experts with powers of two; the choice is within 15% of the faster one.  With fp32 scales both take a little
+// longer: of 148 shapes the choice is the faster one or within 7% of it in 145, within 20% in all.  Here a CTA goes through its part of
 // every expert in turn, there experts are side by side and a tile is 256 rows whatever it holds.
 // 128 x 28672 x 8192 forward 81 against 55 us, 128 x 8192 x 28672 61 against 73, one row 40 against 76;
 // 32 rows of 16 experts, 1024 x 8192, 63 against 33.
-bool grs::fp8_few_serves(Fp8Kind kind, Fp8Scale scale, const Fp8Rows& rows, int64_t N, int64_t Kr, bool with_weight_grad, int sms) {
+bool grs::fp8_few_serves(Fp8Kind kind, const Fp8Rows& rows, int64_t N, int64_t Kr, bool with_weight_grad, int sms) {
   if (rows.M > kFewRows) return false;
   const int64_t E = rows.offsets ? rows.experts : 1;
   // up to 32 M weights one launch for both gradients is faster (128 x 2048 x 4096 42 -> 17.5 us), above it the

@@ -1,21 +1,19 @@
-// fp8_gemm.cu -- products of e4m3 operands with a scale for each block of 128
-// (gemm_rs_fp8_* and gemm_rs_moe_* in include/gemm_rs_ops.h).
+// fp8_gemm.cu -- products of e4m3 operands with a power of two for each block of 128
+// (gemm_rs_fp8_*_e8m0 and gemm_rs_moe_*_e8m0 in include/gemm_rs_ops.h).
 //
 // A step multiplies 128 inner elements.  The elements of a row of A share a power of
 // two in it, and so do those of a column of B, so the tensor cores apply both scales
 // themselves (tcgen05 kind::mxf8f6f4, whose scales are of 32 elements each: a block's
 // byte serves four of them) and sums stay in TMEM for the whole contraction.
 //
-// Tiles of 256 x 256, one at a time for each pair of CTAs (cta_group::2).  Operands
-// are read as they lie in memory, K-major or MN-major, through TMA.  Scales go from
-// registers to shared memory in the layout that tcgen05.cp expects, four steps at a
+// Scales go from registers to shared memory in the layout that tcgen05.cp expects, four steps at a
 // time, and by tcgen05.cp to TMEM.  One accumulator of 256 columns: two would leave no
 // TMEM for scales.  The epilogue therefore first reads all of it into registers (128 of a
 // thread), hands it back, and rounds and stores while the next tile is multiplied.
 // Warps in each CTA: 0 loads A, 2 loads B, 3 brings scales, 1 issues the MMAs (first
 // CTA of the pair), 4 to 11 round and store.
-// Bound by the tensor cores and, repeated, by the power limit: 8192 x 8192 x 28672 forward 1.2 ms
-// with its quantisation, 3.2 PFLOP/s; 2048 x 8192 x 8192 86 us, 256 tiles in four waves of 76.
+// Bound by the tensor cores and, repeated, by the power limit: 8192 x 8192 x 28672 forward 1.21 to 1.41 ms
+// with its quantisation, 2.7 to 3.2 PFLOP/s; 2048 x 8192 x 8192 89 us, 256 tiles in four waves of 76.
 // dA and dW are independent, so a backward pass multiplies both in one launch, dA's tiles
 // first: 392 x 776 x 1600 19.4 -> 12.0 us, 2048 x 8192 x 8192 187 -> 181.
 #include "fp8_tiles.cuh"

@@ -7,10 +7,10 @@
 //   rows: the token-expert pairs in the order of their experts, then tokens
 //   out[t] = sum_j weight[t][j] (A[row] W[expert])     row = rows[t][j]
 //
-// A warp routes a token, lane l the experts l, l + 32, ...  What is chosen does not
-// depend on rounding: without a bias the order of scores is that of the logits;
+// Eight lanes or a whole warp route a token, lane l of them the experts l, l + 8 (or 32), ...  What is
+// chosen does not depend on rounding: without a bias the order of scores is that of the logits;
 // with one, or between groups, two fp32 values that are nearer than their errors
-// send the token through the same code in 64 bits.
+// send the token through the same code in 64 bits, by the whole warp.
 #include <cfloat>
 #include <cstring>
 
@@ -1186,7 +1186,7 @@ int forward(Fp8Scale scale, const gemm_rs_moe_desc* d, const void* A, const void
   q.status = at<uint32_t>(workspace, 0);
   rc = fp8_quantize_rows(q, st);
   if (rc || d->N == 0) return rc;
-  if (fp8_few_serves(kFp8Forward, scale, q.rows, d->N, d->K / kWorld, false, sms)) {
+  if (fp8_few_serves(kFp8Forward, q.rows, d->N, d->K / kWorld, false, sms)) {
     Fp8Few f;
     f.scale = scale;
     f.kind = kFp8Forward;
@@ -1297,7 +1297,7 @@ int backward(Fp8Scale scale, const gemm_rs_moe_desc* d, const void* dout, const 
       q.token_scales = at<void>(workspace, w.token_scales);
     }
     q.status = at<uint32_t>(workspace, 0);
-    const bool few = dA && fp8_few_serves(kFp8InputGrad, scale, q.rows, d->N, d->K / kWorld, dW != nullptr, sms);
+    const bool few = dA && fp8_few_serves(kFp8InputGrad, q.rows, d->N, d->K / kWorld, dW != nullptr, sms);
     rc = fp8_quantize_rows(q, st);
     if (rc) return rc;
     Fp8Product m;
