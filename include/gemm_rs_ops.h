@@ -168,7 +168,7 @@ int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int has_zeros, co
  * well.  experts is 1 for the layer itself.
  *
  * The entries whose names end in _e8m0 are the same in a form that large products
- * take half to two thirds of the time in, for some accuracy: every block's scale, of weights, inputs and
+ * take 0.6 to 0.8 of the time in, for some accuracy: every block's scale, of weights, inputs and
  * gradients alike, is a power of two, 2^e with the least e >= -126 such that the
  * block's largest magnitude is at most 448 * 2^e; codes are the elements over 2^e,
  * and the tensor cores apply the scales, so that the whole contraction is summed in

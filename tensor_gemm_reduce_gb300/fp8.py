@@ -14,7 +14,7 @@ once.  A block with an infinity or a NaN makes NaN of the outputs that it takes 
 A weight of quantize(W, scales=torch.float8_e8m0fnu) has powers of two instead, the
 least whose 448-fold holds the block, and so have the inputs and gradients that are
 multiplied by it.  The tensor cores apply these by themselves: products of many tokens
-take half to two thirds of the time, and are less accurate (inputs with one entry in 20 eight times
+take 0.6 to 0.8 of the time, and are less accurate (inputs with one entry in 20 eight times
 as large are rounded by 2.7% of their norm, with fp32 by 2.1%).
 
 Weights of several experts, W [E][8][K/8][N], are quantised alike; moe.py
