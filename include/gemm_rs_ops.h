@@ -159,7 +159,7 @@ int gemm_rs_w4_run(int64_t M, int64_t N, int64_t K, int group, int has_zeros, co
  * the codes of a step of 128 inner elements are multiplied and summed on the
  * tensor cores in fp32, scaled by the product of the two scales, and added up
  * in fp32 (where the product of two scales is no normal number of fp32, the step loses
- * bits or is infinite); outputs are rounded to bf16 once.  The same call gives the same bits; with
+ * bits, or is infinite or NaN); outputs are rounded to bf16 once.  The same call gives the same bits; with
  * other rows beside it, or for dA without dW, a sum may run in another order.
  *
  * Weights: codes [experts][8][ceil(N/128)][K/8][128] e4m3 (128 columns of W at a
